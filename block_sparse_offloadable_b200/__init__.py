@@ -20,23 +20,27 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "_lib", "libnosa.so")
 _SOURCES = ["nosa_api.cu", "nosa_append.cu", "nosa_select.cu", "nosa_cache.cu", "nosa_decode.cu", "nosa_step.cu",
-            "nosa_noalloc.cu", "nosa_diag.cu"]
-_HEADERS = ["nosa_common.cuh", "nosa_internal.cuh", "nosa_append_unit.cuh", "nosa_attend.cuh"]
+            "nosa_noalloc.cu", "nosa_diag.cu", "nosa_evict.cu"]
+_HEADERS = ["nosa_common.cuh", "nosa_internal.cuh", "nosa_append_unit.cuh", "nosa_attend.cuh", "nosa_attend8.cuh",
+            "nosa_kv8.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
 
 OK, ERR_ARG, ERR_CAPACITY, ERR_PTR, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED, ERR_DEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 EFLAG_CAPACITY, EFLAG_TIMEOUT, EFLAG_NOSLOT, EFLAG_STATE = 1, 2, 4, 8
-FLAG_CK_BF16, FLAG_FILL = 1, 2
+FLAG_CK_BF16, FLAG_FILL, FLAG_KV_INT8, FLAG_KV_E4M3 = 1, 2, 8, 16
+KV_FORMATS = {"bf16": 0, "int8": FLAG_KV_INT8, "e4m3": FLAG_KV_E4M3}
 (BUF_KV_STORE, BUF_EVICT_LOGIT, BUF_CK, BUF_BLK_EVICT, BUF_GAMMA_E, BUF_GAMMA_N, BUF_SEQ_LEN, BUF_CACHE,
  BUF_SLOT_BLOCK, BUF_BLOCK_SLOT, BUF_ERR, BUF_POOL, BUF_POOL_N) = range(13)
 WS_SELECT, WS_SPARSE_DECODE, WS_DENSE_DECODE, WS_CACHE_SYNC, WS_SPLIT, WS_FUSED_STEP = 0, 1, 2, 3, 4, 5
+WS_SPARSE_WEIGHTS, WS_DENSE_WEIGHTS = 6, 7
 
 # Every extern "C" symbol include/nosa.h declares.
 EXPORTS = ["nosa_validate_config", "nosa_state_bytes", "nosa_workspace_bytes", "nosa_state_init",
            "nosa_compress_append", "nosa_compress_append_head", "nosa_select", "nosa_append_select", "nosa_cache_sync", "nosa_sparse_decode",
            "nosa_dense_decode", "nosa_decode_resident", "nosa_decode_rest", "nosa_read_error", "nosa_strerror",
-           "nosa_select_noalloc", "nosa_noalloc_scratch_poison", "nosa_check_wait_timeout", "nosa_fused_step"]
+           "nosa_select_noalloc", "nosa_noalloc_scratch_poison", "nosa_check_wait_timeout", "nosa_fused_step",
+           "nosa_sparse_decode_weights", "nosa_dense_decode_weights", "nosa_evict"]
 NOALLOC_SELECT_SCRATCH = 1 << 20
 
 
@@ -96,6 +100,10 @@ def lib():
         L.nosa_decode_resident.argtypes = [C, S, P, P, ctypes.c_size_t, P, ctypes.c_size_t, P]
         L.nosa_decode_rest.argtypes = [C, S, P, P, P, ctypes.c_size_t, P, P, ctypes.c_size_t, P]
         L.nosa_dense_decode.argtypes = [C, S, P, P, P, ctypes.c_size_t, P]
+        L.nosa_sparse_decode_weights.argtypes = [C, S, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.nosa_dense_decode_weights.argtypes = [C, S, P, P, P, P, ctypes.c_size_t, P]
+        I = ctypes.c_int32
+        L.nosa_evict.argtypes = [C, S, P, I, I, I, C, S, P, P, P]
         L.nosa_read_error.argtypes = [S, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int, P]
         L.nosa_check_wait_timeout.argtypes = [P, ctypes.c_int64, P]
         L.nosa_select_noalloc.argtypes = [C, S, P, P, P, P, P]
@@ -128,10 +136,13 @@ def _stream(stream):
 
 
 def make_config(batch, heads_q, heads_kv, k_q, k_e, max_ctx, offload=False, head_dim=128, block=64, sub_block=16,
-                scale=None, ck_bf16=False, fill=False):
+                scale=None, ck_bf16=False, fill=False, kv_format="bf16"):
+    """kv_format: how the KV store's blocks are held, "bf16", "int8" or "e4m3" (8 bits, a scale per block)."""
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format {kv_format!r}: one of {sorted(KV_FORMATS)}")
     return Config(batch, heads_q, heads_kv, head_dim, block, sub_block, k_q, k_e, 1, int(bool(offload)),
                   int(max_ctx), float(scale if scale is not None else head_dim ** -0.5),
-                  (FLAG_CK_BF16 if ck_bf16 else 0) | (FLAG_FILL if fill else 0))
+                  (FLAG_CK_BF16 if ck_bf16 else 0) | (FLAG_FILL if fill else 0) | KV_FORMATS[kv_format])
 
 
 # ---- the C entry points, one to one -------------------------------------------------
@@ -226,6 +237,23 @@ def nosa_dense_decode(cfg, st, q, out, ws=None, stream=None):
                                    _stream(stream)), "nosa_dense_decode")
 
 
+def nosa_sparse_decode_weights(cfg, st, q, sel, nsel, block_table, out, weights, ws=None, stream=None):
+    _check(lib().nosa_sparse_decode_weights(ctypes.byref(cfg), ctypes.byref(st), _ptr(q), _ptr(sel), _ptr(nsel),
+                                            _ptr(block_table), _ptr(out), _ptr(weights), _ptr(ws), _nbytes(ws),
+                                            _stream(stream)), "nosa_sparse_decode_weights")
+
+
+def nosa_dense_decode_weights(cfg, st, q, out, weights, ws=None, stream=None):
+    _check(lib().nosa_dense_decode_weights(ctypes.byref(cfg), ctypes.byref(st), _ptr(q), _ptr(out), _ptr(weights),
+                                           _ptr(ws), _nbytes(ws), _stream(stream)), "nosa_dense_decode_weights")
+
+
+def nosa_evict(cfg, st, weights, keep, sink, recent, dst_cfg, dst, dst_weights, kept, stream=None):
+    _check(lib().nosa_evict(ctypes.byref(cfg), ctypes.byref(st), _ptr(weights), int(keep), int(sink), int(recent),
+                            ctypes.byref(dst_cfg), ctypes.byref(dst), _ptr(dst_weights), _ptr(kept),
+                            _stream(stream)), "nosa_evict")
+
+
 def nosa_check_wait_timeout(err, max_cycles, stream=None):
     """Run the bounded-wait diagnostic into the device word `err` (a 1-element int32 tensor)."""
     _check(lib().nosa_check_wait_timeout(_ptr(err), int(max_cycles), _stream(stream)), "nosa_check_wait_timeout")
@@ -246,9 +274,11 @@ class NosaLayer:
 
     ``host_store``: in offload mode, an existing pinned uint8 tensor to use as the host KV store
     (several layers may share one when their synthetic KV is identical); allocated if None.
+    ``weights``: keep a running total of each block's attention weight (``self.weights`` fp32
+    [units][blocks]); ``decode_step`` then adds to it.
     """
 
-    def __init__(self, cfg, device="cuda", host_store=None):
+    def __init__(self, cfg, device="cuda", host_store=None, weights=False):
         rc = nosa_validate_config(cfg)
         if rc != OK:
             raise NosaError(rc, "config")
@@ -304,6 +334,11 @@ class NosaLayer:
         self.ws_cache = ws(WS_CACHE_SYNC)
         self.split = None if cfg.flags & FLAG_FILL else ws(WS_SPLIT)
         self.ws_step = ws(WS_FUSED_STEP)
+        self.weights = self.ws_sparse_weights = self.ws_dense_weights = None
+        if weights:
+            self.weights = torch.zeros((self.units, cfg.max_ctx // cfg.block), dtype=torch.float32, device=dev)
+            self.ws_sparse_weights = ws(WS_SPARSE_WEIGHTS)
+            self.ws_dense_weights = ws(WS_DENSE_WEIGHTS)
         nosa_state_init(cfg, self.state)
 
     # one decode step = the four calls, in order
@@ -341,17 +376,65 @@ class NosaLayer:
     def dense_decode(self, q, out, stream=None):
         nosa_dense_decode(self.cfg, self.state, q, out, self.ws_dense, stream)
 
+    def _need_weights(self):
+        if self.weights is None:
+            raise ValueError("NosaLayer(..., weights=True) keeps the blocks' weights")
+
+    def sparse_decode_weights(self, q, out, stream=None):
+        """sparse_decode, adding each attended block's weight to ``weights``."""
+        self._need_weights()
+        bt = self.block_table if self.cfg.offload else None
+        nosa_sparse_decode_weights(self.cfg, self.state, q, self.sel, self.nsel, bt, out, self.weights,
+                                   self.ws_sparse_weights, stream)
+
+    def dense_decode_weights(self, q, out, stream=None):
+        """dense_decode, adding each block's weight to ``weights``."""
+        self._need_weights()
+        nosa_dense_decode_weights(self.cfg, self.state, q, out, self.weights, self.ws_dense_weights, stream)
+
+    def evict(self, dst, keep, sink=0, recent=0, stream=None):
+        """Move the ``keep`` candidate blocks per unit with the largest ``weights`` (the first ``sink``
+        and the last ``recent`` always) and the local block into the layer ``dst``, which takes over
+        the sequences.  Returns the kept blocks' numbers, int32 [units][keep + 1], -1 padded."""
+        self._need_weights()
+        dst._need_weights()
+        kept = torch.empty((self.units, max(int(keep), 0) + 1), dtype=torch.int32, device=self.device)
+        nosa_evict(self.cfg, self.state, self.weights, keep, sink, recent, dst.cfg, dst.state, dst.weights, kept,
+                   stream)
+        return kept
+
+    def kv8_views(self):
+        """An 8-bit layer's codes (int8 or float8_e4m3fn [units][blocks][2][64][D], device store; the cache's
+        [units][slots]... with offload), scales [units][blocks][2] and bf16 tails [units][2][64][D]."""
+        cfg = self.cfg
+        if not cfg.flags & (FLAG_KV_INT8 | FLAG_KV_E4M3):
+            raise ValueError("kv8_views: the layer's KV store is bf16")
+        buf = self.cache if cfg.offload else self.kv_store
+        nblk = cfg.max_ctx // cfg.block
+        held = cfg.k_q + cfg.k_e + 2 if cfg.offload else nblk
+        n2 = (nblk + 1) // 2 * 2
+        codes, scales = self.units * held * 2 * 64 * 128, self.units * n2 * 8
+        dtype = torch.int8 if cfg.flags & FLAG_KV_INT8 else torch.float8_e4m3fn
+        tail = codes + (scales + 255) // 256 * 256
+        return (buf[:codes].view(dtype).view(self.units, held, 2, 64, 128),
+                buf[codes:codes + scales].view(torch.float32).view(self.units, n2, 2)[:, :nblk],
+                buf[tail:tail + self.units * 32768].view(torch.bfloat16).view(self.units, 2, 64, 128))
+
     def decode_step(self, k_new, v_new, e_new, q, out, stream=None):
         """One decode step of this layer into `out` (bf16 bits [B][Hq][D]): with the KV store in
         device memory and the union reading, nosa_fused_step (one launch); otherwise append +
-        select in one launch, the cache sync (offload), and the sparse decode."""
-        if self.ws_step is not None:
+        select in one launch, the cache sync (offload), and the sparse decode (which, in a layer
+        with ``weights``, adds the blocks' weights)."""
+        if self.ws_step is not None and self.weights is None:
             self.fused_step(k_new, v_new, e_new, q, out, stream)
             return
         self.append_select(k_new, v_new, e_new, q, stream)
         if self.cfg.offload:
             self.cache_sync(stream)
-        self.sparse_decode(q, out, stream)
+        if self.weights is None:
+            self.sparse_decode(q, out, stream)
+        else:
+            self.sparse_decode_weights(q, out, stream)
 
     def fused_step(self, k_new, v_new, e_new, q, out, stream=None):
         """One decode step of this layer in one launch (device store, union reading): append,

@@ -12,6 +12,7 @@ using namespace nosa;
 namespace {
 
 constexpr int64_t kMaxCtx = 1ll << 20;
+constexpr int32_t kKv8Flags = NOSA_FLAG_KV_INT8 | NOSA_FLAG_KV_E4M3;
 
 struct Geo {
     int64_t units, nblk, nsub, nslots, max_sel, G;
@@ -27,6 +28,12 @@ bool geo_of(const nosa_config *c, Geo *g) {
     g->G = c->heads_q / c->heads_kv;
     return true;
 }
+
+int fmt_of(const nosa_config *c) {
+    return (c->flags & NOSA_FLAG_KV_INT8) ? kFmtInt8 : (c->flags & NOSA_FLAG_KV_E4M3) ? kFmtE4m3 : kFmtBf16;
+}
+
+size_t block_bytes(const nosa_config *c) { return fmt_of(c) == kFmtBf16 ? kBlockBytes : kBlock8Bytes; }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -69,6 +76,32 @@ int store_addr(const nosa_config *c, const nosa_state *st, uint8_t **out) {
     return NOSA_OK;
 }
 
+// The 8-bit store's scales and tails, behind the blocks of codes in the buffer that is in device memory
+// (kv_store, or the block cache with offload).  base may be null: the sizes alone.
+struct Kv8Region {
+    size_t scales, tail, total;
+};
+
+Kv8Region kv8_region(const nosa_config *c, const Geo &g) {
+    Kv8Region r;
+    const size_t u = (size_t)g.units;
+    r.scales = u * (size_t)(c->offload ? g.nslots : g.nblk) * kBlock8Bytes;
+    r.tail = r.scales + align256(u * (size_t)((g.nblk + 1) & ~1ll) * sizeof(float2));
+    r.total = r.tail + u * kBlockBytes;
+    return r;
+}
+
+Kv8 kv8_of(const nosa_config *c, const Geo &g, const nosa_state *st) {
+    Kv8 k = {};
+    if (fmt_of(c) == kFmtBf16) return k;
+    uint8_t *base = static_cast<uint8_t *>(c->offload ? st->cache : st->kv_store);
+    const Kv8Region r = kv8_region(c, g);
+    k.scales = reinterpret_cast<float2 *>(base + r.scales);
+    k.tail = base + r.tail;
+    k.scale_stride = (int32_t)((g.nblk + 1) & ~1ll);
+    return k;
+}
+
 int check_state(const nosa_config *c, const nosa_state *st) {
     if (!st) return NOSA_ERR_ARG;
     int rc;
@@ -101,18 +134,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Tensor map over a block-major KV buffer seen as [rows][128] bf16 rows,
-// box = 64 rows x 64 dims (128 bytes), 128-byte swizzle.
-int kv_tensor_map(CUtensorMap *map, const void *base, int64_t rows) {
+// Tensor map over a block-major KV buffer seen as [rows][128] rows of bf16 (box = 64 rows x 64 dims)
+// or of codes (64 rows x 128 dims): 128 bytes wide either way, 128-byte swizzle.
+int kv_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int fmt = kFmtBf16) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return NOSA_ERR_CUDA;
+    const bool k8 = fmt != kFmtBf16;
     cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)kRowBytes};
-    cuuint32_t box[2] = {64, 64};
+    cuuint64_t strides[1] = {(cuuint64_t)(k8 ? kRow8Bytes : kRowBytes)};
+    cuuint32_t box[2] = {k8 ? 128u : 64u, 64};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims,
-                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = enc(map, k8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                     const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? NOSA_OK : NOSA_ERR_CUDA;
 }
 
@@ -144,6 +179,12 @@ StepWs step_ws(const nosa_config *c, const Geo &g) {
     return w;
 }
 
+// Counters and partial states of a decode, padded: the items' weights follow.
+size_t decode_ws_bytes(const Geo &g) {
+    return align256((size_t)g.units * sizeof(int32_t)) +
+           align256((size_t)decode_ctas() * 2 * kPartFloats * sizeof(float));
+}
+
 size_t ws_bytes_of(const nosa_config *c, int which) {
     Geo g;
     if (!geo_of(c, &g)) return 0;
@@ -153,14 +194,19 @@ size_t ws_bytes_of(const nosa_config *c, int which) {
         return n > 1 ? counters + (size_t)g.units * n * 32 * sizeof(uint64_t) : 0;
     }
     if (which == NOSA_WS_SPARSE_DECODE || which == NOSA_WS_DENSE_DECODE)
-        return counters + (size_t)decode_ctas() * 2 * kPartFloats * sizeof(float);
+        return counters + (size_t)decode_ctas() * 2 * kPartFloats * sizeof(float);  // = decode_ws_bytes, unpadded
+    if (which == NOSA_WS_SPARSE_WEIGHTS || which == NOSA_WS_DENSE_WEIGHTS) {
+        if (which == NOSA_WS_DENSE_WEIGHTS && c->offload) return 0;
+        const size_t items = (size_t)g.units * (which == NOSA_WS_SPARSE_WEIGHTS ? g.max_sel : g.nblk);
+        return decode_ws_bytes(g) + items * kRecFloats * sizeof(float);
+    }
     if (which == NOSA_WS_CACHE_SYNC)
         return c->offload ? counters + (size_t)g.units * g.max_sel * sizeof(uint32_t) : 0;
     if (which == NOSA_WS_SPLIT)
         return align256((size_t)g.units * kPartFloats * sizeof(float)) +
                (size_t)g.units * split_bits_words(g) * sizeof(uint32_t);
     if (which == NOSA_WS_FUSED_STEP) {
-        if (c->offload || (c->flags & NOSA_FLAG_FILL)) return 0;
+        if (c->offload || (c->flags & NOSA_FLAG_FILL) || fmt_of(c) != kFmtBf16) return 0;
         const StepWs w = step_ws(c, g);
         return w.total;
     }
@@ -178,7 +224,7 @@ int check_ws(const nosa_config *c, int which, void *ws, size_t ws_bytes) {
 // live, and where the result goes differ; see nosa_decode.cu.
 int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, int mode, const int32_t *sel,
                const int32_t *nsel, const int32_t *block_table, const int32_t *gq, void *split,
-               size_t split_bytes, uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
+               size_t split_bytes, uint16_t *out, float *weights, void *ws, size_t ws_bytes, void *stream) {
     Geo g;
     int rc;
     if ((rc = nosa_validate_config(c))) return rc;
@@ -195,7 +241,9 @@ int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, in
         if ((rc = check_ws(c, NOSA_WS_SPLIT, split, split_bytes))) return rc;
         if (mode == kModeRest && c->k_q > 0 && (rc = check_dev(gq, false))) return rc;
     }
-    const int which = mode == kModeDense ? NOSA_WS_DENSE_DECODE : NOSA_WS_SPARSE_DECODE;
+    const int which = weights ? (mode == kModeDense ? NOSA_WS_DENSE_WEIGHTS : NOSA_WS_SPARSE_WEIGHTS)
+                              : (mode == kModeDense ? NOSA_WS_DENSE_DECODE : NOSA_WS_SPARSE_DECODE);
+    if (weights && (rc = check_dev(weights, false))) return rc;
     if ((rc = check_ws(c, which, ws, ws_bytes))) return rc;
 
     const void *base;
@@ -209,11 +257,22 @@ int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, in
         base = s;
         bpu = g.nblk;
     }
-    CUtensorMap map;
-    if ((rc = kv_tensor_map(&map, base, g.units * bpu * 2 * kBlock))) return rc;
+    const int fmt = fmt_of(c);
+    CUtensorMap map, tail_map;
+    if ((rc = kv_tensor_map(&map, base, g.units * bpu * 2 * kBlock, fmt))) return rc;
+    tail_map = map;
+    const Kv8 kv8 = kv8_of(c, g, st);
+    if (fmt != kFmtBf16 && (rc = kv_tensor_map(&tail_map, kv8.tail, g.units * 2 * kBlock))) return rc;
 
     DecodeParams p;
     memset(&p, 0, sizeof(p));
+    p.fmt = fmt;
+    p.kv8 = kv8;
+    p.nblk = (int32_t)g.nblk;
+    if (weights) {
+        p.weights = weights;
+        p.rec = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + decode_ws_bytes(g));
+    }
     p.q = q;
     p.mode = mode;
     p.sel = mode == kModeSel ? sel : nullptr;
@@ -223,7 +282,6 @@ int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, in
         p.gamma_e = st->gamma_e; p.gamma_n = st->gamma_n; p.k_e = c->k_e;
         p.gq = c->k_q > 0 ? gq : nullptr; p.k_q = c->k_q;
         p.block_slot = c->offload ? st->block_slot : nullptr;
-        p.nblk = (int32_t)g.nblk;
         p.bits_words = (int32_t)split_bits_words(g);
         p.res_part = static_cast<float *>(split);
         p.res_bits = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(split) +
@@ -246,7 +304,7 @@ int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, in
     // instead of stalling mid-stream on the hand-off of a unit it shares with its neighbour.
     if (mode == kModeSel && g.units <= decode_ctas())
         p.pieces = (int32_t)std::min<int64_t>(decode_ctas() / g.units, g.max_sel);
-    return launch_decode(p, map, static_cast<cudaStream_t>(stream));
+    return launch_decode(p, map, tail_map, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -257,7 +315,8 @@ int nosa_validate_config(const nosa_config *c) {
     if (!c) return NOSA_ERR_ARG;
     if (c->batch < 1 || c->heads_kv < 1 || c->heads_q < 1 || c->heads_q % c->heads_kv) return NOSA_ERR_ARG;
     if (c->k_q < 0 || c->k_e < 0 || c->k_q + c->k_e < 1 || c->max_ctx <= 0 ||
-        c->max_ctx % 64 || (c->flags & ~(NOSA_FLAG_CK_BF16 | NOSA_FLAG_FILL)) != 0 || !(c->scale > 0.f) || !isfinite(c->scale))
+        c->max_ctx % 64 || (c->flags & ~(NOSA_FLAG_CK_BF16 | NOSA_FLAG_FILL | kKv8Flags)) != 0 ||
+        (c->flags & kKv8Flags) == kKv8Flags || !(c->scale > 0.f) || !isfinite(c->scale))
         return NOSA_ERR_ARG;
     if (c->offload != 0 && c->offload != 1) return NOSA_ERR_ARG;
     if (c->head_dim != kD || c->block != kBlock || c->sub_block != kSub || c->local_blocks != 1)
@@ -277,14 +336,17 @@ size_t nosa_state_bytes(const nosa_config *c, int which) {
     if (!geo_of(c, &g)) return 0;
     const size_t u = (size_t)g.units;
     switch (which) {
-    case NOSA_BUF_KV_STORE: return u * g.nblk * kBlockBytes;
+    case NOSA_BUF_KV_STORE:
+        return fmt_of(c) != kFmtBf16 && !c->offload ? kv8_region(c, g).total : u * g.nblk * block_bytes(c);
     case NOSA_BUF_EVICT_LOGIT: return u * c->max_ctx * sizeof(float);
     case NOSA_BUF_CK: return u * g.nsub * kD * ((c->flags & NOSA_FLAG_CK_BF16) ? 2 : sizeof(float));
     case NOSA_BUF_BLK_EVICT: return u * g.nblk * sizeof(double);
     case NOSA_BUF_GAMMA_E: return u * (c->k_e > 0 ? c->k_e : 1) * sizeof(int32_t);
     case NOSA_BUF_GAMMA_N:
     case NOSA_BUF_SEQ_LEN: return u * sizeof(int32_t);
-    case NOSA_BUF_CACHE: return c->offload ? u * g.nslots * kBlockBytes : 0;
+    case NOSA_BUF_CACHE:
+        if (!c->offload) return 0;
+        return fmt_of(c) != kFmtBf16 ? kv8_region(c, g).total : u * g.nslots * kBlockBytes;
     case NOSA_BUF_SLOT_BLOCK: return c->offload ? u * g.nslots * sizeof(int32_t) : 0;
     case NOSA_BUF_BLOCK_SLOT: return c->offload ? u * g.nblk * sizeof(int32_t) : 0;
     case NOSA_BUF_ERR: return sizeof(uint32_t);
@@ -356,6 +418,8 @@ int make_append(const nosa_config *c, const nosa_state *st, const uint16_t *k_ne
     p.offload = c->offload; p.T = T; p.ck_bf16 = (c->flags & NOSA_FLAG_CK_BF16) != 0;
     p.fill = (c->flags & NOSA_FLAG_FILL) != 0;
     p.pool = p.fill ? st->pool : nullptr; p.pool_n = p.fill ? st->pool_n : nullptr;
+    p.fmt = fmt_of(c);
+    p.kv8 = kv8_of(c, g, st);
     *out = p;
     return NOSA_OK;
 }
@@ -442,7 +506,7 @@ int nosa_fused_step(const nosa_config *c, const nosa_state *st, const uint16_t *
                     void *ws, size_t ws_bytes, void *stream) {
     int rc;
     if ((rc = nosa_validate_config(c))) return rc;
-    if (c->offload || (c->flags & NOSA_FLAG_FILL)) return NOSA_ERR_UNSUPPORTED;
+    if (c->offload || (c->flags & NOSA_FLAG_FILL) || fmt_of(c) != kFmtBf16) return NOSA_ERR_UNSUPPORTED;
     if (!e_new) return NOSA_ERR_ARG;
     AppendParams a;
     if ((rc = make_append(c, st, k_new, v_new, e_new, nullptr, nullptr, 1, nullptr, &a))) return rc;
@@ -521,33 +585,106 @@ int nosa_cache_sync(const nosa_config *c, const nosa_state *st, const int32_t *s
                                                align256((size_t)g.units * sizeof(int32_t)));
     p.nblk = (int32_t)g.nblk; p.nslots = (int32_t)g.nslots; p.units = (int32_t)g.units;
     p.max_sel = (int32_t)g.max_sel;
+    p.fmt = fmt_of(c);
     return launch_cache_sync(p, static_cast<cudaStream_t>(stream));
 }
 
 int nosa_sparse_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q,
                        const int32_t *sel, const int32_t *nsel, const int32_t *block_table,
                        uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
-    return run_decode(c, st, q, kModeSel, sel, nsel, block_table, nullptr, nullptr, 0, out, ws, ws_bytes, stream);
+    return run_decode(c, st, q, kModeSel, sel, nsel, block_table, nullptr, nullptr, 0, out, nullptr, ws, ws_bytes, stream);
 }
 
 int nosa_decode_resident(const nosa_config *c, const nosa_state *st, const uint16_t *q, void *split,
                          size_t split_bytes, void *ws, size_t ws_bytes, void *stream) {
     return run_decode(c, st, q, kModeResident, nullptr, nullptr, nullptr, nullptr, split, split_bytes, nullptr,
-                      ws, ws_bytes, stream);
+                      nullptr, ws, ws_bytes, stream);
 }
 
 int nosa_decode_rest(const nosa_config *c, const nosa_state *st, const uint16_t *q, const int32_t *gq,
                      const void *split, size_t split_bytes, uint16_t *out, void *ws, size_t ws_bytes,
                      void *stream) {
     return run_decode(c, st, q, kModeRest, nullptr, nullptr, nullptr, gq, const_cast<void *>(split), split_bytes,
-                      out, ws, ws_bytes, stream);
+                      out, nullptr, ws, ws_bytes, stream);
 }
 
 int nosa_dense_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q,
                       uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
     if (c && c->offload) return NOSA_ERR_ARG;
-    return run_decode(c, st, q, kModeDense, nullptr, nullptr, nullptr, nullptr, nullptr, 0, out, ws, ws_bytes,
+    return run_decode(c, st, q, kModeDense, nullptr, nullptr, nullptr, nullptr, nullptr, 0, out, nullptr, ws, ws_bytes,
                       stream);
+}
+
+int nosa_sparse_decode_weights(const nosa_config *c, const nosa_state *st, const uint16_t *q, const int32_t *sel,
+                               const int32_t *nsel, const int32_t *block_table, uint16_t *out, float *weights,
+                               void *ws, size_t ws_bytes, void *stream) {
+    if (!weights) return NOSA_ERR_PTR;
+    return run_decode(c, st, q, kModeSel, sel, nsel, block_table, nullptr, nullptr, 0, out, weights, ws, ws_bytes,
+                      stream);
+}
+
+int nosa_dense_decode_weights(const nosa_config *c, const nosa_state *st, const uint16_t *q, uint16_t *out,
+                              float *weights, void *ws, size_t ws_bytes, void *stream) {
+    if (c && c->offload) return NOSA_ERR_ARG;
+    if (!weights) return NOSA_ERR_PTR;
+    return run_decode(c, st, q, kModeDense, nullptr, nullptr, nullptr, nullptr, nullptr, 0, out, weights, ws,
+                      ws_bytes, stream);
+}
+
+int nosa_evict(const nosa_config *c, const nosa_state *st, const float *weights, int32_t keep, int32_t sink,
+               int32_t recent, const nosa_config *dc, const nosa_state *dst, float *dst_weights, int32_t *kept,
+               void *stream) {
+    Geo g, dg;
+    int rc;
+    if ((rc = nosa_validate_config(c)) || (rc = nosa_validate_config(dc))) return rc;
+    if (c->offload || dc->offload) return NOSA_ERR_UNSUPPORTED;  // the block cache evicts by slots
+    if (c->batch != dc->batch || c->heads_q != dc->heads_q || c->heads_kv != dc->heads_kv || c->k_q != dc->k_q ||
+        c->k_e != dc->k_e || c->flags != dc->flags)
+        return NOSA_ERR_ARG;
+    if (sink < 0 || recent < 0 || keep < 0 || (int64_t)sink + recent > keep) return NOSA_ERR_ARG;
+    geo_of(c, &g);
+    geo_of(dc, &dg);
+    if (keep >= dg.nblk) return NOSA_ERR_CAPACITY;
+    if ((rc = check_state(c, st)) || (rc = check_state(dc, dst))) return rc;
+    if ((rc = check_dev(weights, false)) || (rc = check_dev(dst_weights, false)) || (rc = check_dev(kept, false)))
+        return rc;
+    uint8_t *s, *d;
+    if ((rc = store_addr(c, st, &s)) || (rc = store_addr(dc, dst, &d))) return rc;
+    // the two states must be apart: blocks are moved by many CTAs in no order
+    const auto apart = [](const void *a, size_t na, const void *b, size_t nb) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return !a || !b || x + na <= y || y + nb <= x;
+    };
+    const void *from[NOSA_BUF_COUNT] = {st->kv_store, st->evict_logit, st->ck, st->blk_evict, st->gamma_e, st->gamma_n,
+                                        st->seq_len, nullptr, nullptr, nullptr, nullptr, st->pool, st->pool_n};
+    const void *to[NOSA_BUF_COUNT] = {dst->kv_store, dst->evict_logit, dst->ck, dst->blk_evict, dst->gamma_e,
+                                      dst->gamma_n, dst->seq_len, nullptr, nullptr, nullptr, nullptr, dst->pool,
+                                      dst->pool_n};
+    for (int i = 0; i < NOSA_BUF_COUNT; ++i)
+        if (!apart(from[i], nosa_state_bytes(c, i), to[i], nosa_state_bytes(dc, i))) return NOSA_ERR_ARG;
+    if (!apart(weights, (size_t)(g.units * g.nblk) * sizeof(float), dst_weights,
+               (size_t)(dg.units * dg.nblk) * sizeof(float)))
+        return NOSA_ERR_ARG;
+    EvictParams p;
+    memset(&p, 0, sizeof(p));
+    p.weights = weights;
+    p.seq_len = st->seq_len; p.gamma_e = st->gamma_e; p.gamma_n = st->gamma_n;
+    p.store = s; p.ck = static_cast<const uint8_t *>(st->ck); p.e = st->evict_logit; p.blk_evict = st->blk_evict;
+    p.kv8 = kv8_of(c, g, st); p.dst_kv8 = kv8_of(dc, dg, dst);
+    p.kept = kept;
+    p.dst_weights = dst_weights;
+    p.dst_seq_len = dst->seq_len; p.dst_gamma_e = dst->gamma_e; p.dst_gamma_n = dst->gamma_n;
+    if (c->flags & NOSA_FLAG_FILL) {
+        p.pool = st->pool; p.pool_n = st->pool_n;
+        p.dst_pool = dst->pool; p.dst_pool_n = dst->pool_n;
+    }
+    p.dst_store = d; p.dst_ck = static_cast<uint8_t *>(dst->ck); p.dst_e = dst->evict_logit;
+    p.dst_blk_evict = dst->blk_evict;
+    p.max_ctx = c->max_ctx; p.dst_max_ctx = dc->max_ctx;
+    p.nblk = (int32_t)g.nblk; p.dst_nblk = (int32_t)dg.nblk; p.units = (int32_t)g.units;
+    p.keep = keep; p.sink = sink; p.recent = recent; p.k_e = c->k_e;
+    p.fmt = fmt_of(c); p.ck_bf16 = (c->flags & NOSA_FLAG_CK_BF16) != 0;
+    return launch_evict(p, static_cast<cudaStream_t>(stream));
 }
 
 int nosa_read_error(const nosa_state *st, uint32_t *flags, int clear, void *stream) {

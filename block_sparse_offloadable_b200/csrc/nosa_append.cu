@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(128) append_decode_kernel(const AppendParams p
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int u = blockIdx.x * (blockDim.x >> 5) + warp;
     if (u >= p.units) return;
-    append_unit(p, u, lane, p.e_new[u]);
+    if (p.fmt == kFmtBf16) append_unit<false>(p, u, lane, p.e_new[u]);
+    else append_unit<true>(p, u, lane, p.e_new[u]);
 }
 
 // With the fused eviction head: one CTA of kHeadH threads per unit.  One bulk
@@ -82,7 +83,10 @@ __global__ void __launch_bounds__(kHeadH) append_head_decode_kernel(const Append
         s_e = __double2float_rn(e);
     }
     __syncthreads();
-    if (threadIdx.x < 32) append_unit(p, u, lane, s_e);
+    if (threadIdx.x < 32) {
+        if (p.fmt == kFmtBf16) append_unit<false>(p, u, lane, s_e);
+        else append_unit<true>(p, u, lane, s_e);
+    }
 }
 
 // ---- prefill ----------------------------------------------------------------------
@@ -152,6 +156,124 @@ __global__ void __launch_bounds__(256) prefill_pool_kernel(const AppendParams p)
             m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
             if (lane == 0) p.blk_evict[(int64_t)u * p.nblk + blk] = m;
         }
+    }
+}
+
+// A block's rows (bf16, in the registers of a CTA of 256 threads: thread's piece i is piece
+// tid + 256 i of the keys and of the values) to codes at dst; returns the scales.  Two barriers.
+__device__ __forceinline__ float2 code_block(const uint4 (&k)[4], const uint4 (&v)[4], uint8_t *dst,
+                                             uint32_t (*s_max)[8], int fmt) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t ak = 0, av = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        ak = absmax4(ak, k[i]);
+        av = absmax4(av, v[i]);
+    }
+    ak = absmax_warp(ak);
+    av = absmax_warp(av);
+    __syncthreads();  // s_max may still be read from the block before
+    if (lane == 0) {
+        s_max[0][warp] = ak;
+        s_max[1][warp] = av;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        ak = max(ak, s_max[0][i]);
+        av = max(av, s_max[1][i]);
+    }
+    const float2 sk = scale_of(ak, fmt), sv = scale_of(av, fmt);
+    uint2 *to = reinterpret_cast<uint2 *>(dst) + tid;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        to[256 * i] = code8(k[i], sk.y, fmt);
+        to[kHalfBlock8Bytes / 8 + 256 * i] = code8(v[i], sv.y, fmt);
+    }
+    return make_float2(sk.x, sv.x);
+}
+
+// The same two steps for the 8-bit store, in one pass over the input: one CTA per block stages its
+// rows in registers (8 pieces of 16 bytes a thread), finds both largest magnitudes, and writes the
+// codes; the keys also go to shared memory, where the pooled means are summed (thread = sub-block
+// and pair of dims, in row order).  The newest block's rows go to the tail as they are.  Reads
+// 33 KiB and writes 19 KiB a block; bound by HBM.
+__global__ void __launch_bounds__(256) prefill_store8_kernel(const AppendParams p) {
+    __shared__ __align__(16) uint8_t ks[kHalfBlockBytes];
+    __shared__ uint32_t s_max[2][8];
+    __shared__ float s_e[kBlock];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t bpu = (p.T + kBlock - 1) / kBlock;
+    const int32_t u = (int32_t)(blockIdx.x / bpu), blk = (int32_t)(blockIdx.x % bpu);
+    const int32_t len = unit_len(p, u);
+    const int32_t rows = min(len - blk * kBlock, kBlock);
+    if (rows <= 0 || p.seq_len[u] != 0) return;
+    const bool local = blk == (len - 1) >> 6;
+    const int64_t row0 = (int64_t)u * p.T + (int64_t)blk * kBlock;
+    const uint4 *K = reinterpret_cast<const uint4 *>(p.k_new + row0 * kD);
+    const uint4 *V = reinterpret_cast<const uint4 *>(p.v_new + row0 * kD);
+    uint4 k[4], v[4];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // piece tid + 256 i: row (tid >> 4) + 16 i
+        const bool in = (tid >> 4) + 16 * i < rows;
+        k[i] = in ? __ldcs(K + tid + 256 * i) : zero;
+        v[i] = in ? __ldcs(V + tid + 256 * i) : zero;
+    }
+    if (tid < rows) {
+        const float *src = p.w1 ? p.e_store + (int64_t)u * p.max_ctx + blk * kBlock : p.e_new + row0;
+        const float e = src[tid];
+        s_e[tid] = e;
+        if (!p.w1) p.e_store[(int64_t)u * p.max_ctx + blk * kBlock + tid] = e;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(ks)[tid + 256 * i] = k[i];
+    __syncthreads();
+    if (local) {
+        uint4 *tail = reinterpret_cast<uint4 *>(p.kv8.tail + (int64_t)u * kBlockBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((tid >> 4) + 16 * i < rows) {
+                tail[tid + 256 * i] = k[i];
+                tail[kHalfBlockBytes / 16 + tid + 256 * i] = v[i];
+            }
+    } else {
+        const float2 sc = code_block(k, v, p.store + ((int64_t)u * p.nblk + blk) * kBlock8Bytes, s_max, p.fmt);
+        if (tid == 0) p.kv8.scales[(int64_t)u * p.kv8.scale_stride + blk] = sc;
+    }
+    // pooled keys: thread = (sub-block, pair of dims)
+    const int sub = tid >> 6, pair = tid & 63;
+    if ((sub + 1) * kSub <= rows) {
+        const uint32_t *kp = reinterpret_cast<const uint32_t *>(ks) + sub * kSub * (kD / 2) + pair;
+        double a0 = 0.0, a1 = 0.0;
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+            const uint32_t w = kp[j * (kD / 2)];
+            a0 += bf16_lo(w);
+            a1 += bf16_hi(w);
+        }
+        const int64_t row = (int64_t)u * p.nsub + blk * kSubPerBlock + sub;
+        if (p.ck_bf16) {
+            const __nv_bfloat16 b0 = __double2bfloat16(a0 / kSub), b1 = __double2bfloat16(a1 / kSub);
+            reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.ck) + row * kD)[pair] =
+                (uint32_t)*reinterpret_cast<const uint16_t *>(&b0) |
+                ((uint32_t)*reinterpret_cast<const uint16_t *>(&b1) << 16);
+        } else {
+            reinterpret_cast<float2 *>(static_cast<float *>(p.ck) + row * kD)[pair] =
+                make_float2((float)(a0 / kSub), (float)(a1 / kSub));
+        }
+    }
+    // eviction score of a whole block
+    if (warp == 0 && rows == kBlock) {
+        double m = -__longlong_as_double(0x7FF0000000000000ll);
+        if (lane < kSubPerBlock) {
+            double acc = 0.0;
+            for (int j = 0; j < kSub; ++j) acc += (double)s_e[lane * kSub + j];
+            m = acc / kSub;
+        }
+        m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        if (lane == 0) p.blk_evict[(int64_t)u * p.nblk + blk] = m;
     }
 }
 
@@ -234,6 +356,7 @@ __global__ void __launch_bounds__(256) prefill_head_kernel(const AppendParams p)
 // the candidates held in shared memory (the ranks are a permutation).
 __global__ void __launch_bounds__(256) prefill_gamma_kernel(const AppendParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint32_t s_max[2][8];
     const int32_t u = blockIdx.x;
     if (p.seq_len[u] != 0) {
         if (threadIdx.x == 0) set_error(p.err, NOSA_EFLAG_STATE);
@@ -297,6 +420,21 @@ __global__ void __launch_bounds__(256) prefill_gamma_kernel(const AppendParams p
         __syncthreads();
         const int32_t n = min(p.gamma_n[u], p.k_e);
         const int32_t *ge = p.gamma_e + (int64_t)u * p.k_e;
+        if (p.fmt != kFmtBf16) {  // the stored codes are in host memory by now: code the rows again
+            for (int j = 0; j < n; ++j) {
+                const int64_t r0 = ((int64_t)u * p.T + (int64_t)ge[j] * kBlock) * kD;
+                const uint4 *K = reinterpret_cast<const uint4 *>(p.k_new + r0) + threadIdx.x;
+                const uint4 *V = reinterpret_cast<const uint4 *>(p.v_new + r0) + threadIdx.x;
+                uint4 k[4], v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    k[i] = K[256 * i];
+                    v[i] = V[256 * i];
+                }
+                code_block(k, v, p.cache + ((int64_t)u * p.nslots + 1 + j) * kBlock8Bytes, s_max, p.fmt);
+            }
+            return;
+        }
         constexpr int kChunks = kBlockBytes / 16, kHalfChunks = kHalfBlockBytes / 16, kRowChunks = kRowBytes / 16;
         for (int j = 0; j < n; ++j) {
             const int32_t b = ge[j];
@@ -329,10 +467,7 @@ int launch_append(const AppendParams &p, cudaStream_t stream) {
                    ? NOSA_OK
                    : NOSA_ERR_CUDA;
     }
-    const int64_t rows = (int64_t)p.units * p.T;
-    int64_t g = (rows + 7) / 8;
-    if (g > 148 * 16) g = 148 * 16;
-    prefill_store_kernel<<<(unsigned)g, 256, 0, stream>>>(p);
+    const int64_t items = (int64_t)p.units * ((p.T + kBlock - 1) / kBlock);
     if (p.w1) {
         if (cudaFuncSetAttribute(prefill_head_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kHeadSmem) != cudaSuccess)
@@ -340,10 +475,17 @@ int launch_append(const AppendParams &p, cudaStream_t stream) {
         dim3 hg((p.T + kHeadCtaRows - 1) / kHeadCtaRows, p.units);
         prefill_head_kernel<<<hg, 256, kHeadSmem, stream>>>(p);
     }
-    const int64_t items = (int64_t)p.units * ((p.T + kBlock - 1) / kBlock);
-    g = (items + 7) / 8;
-    if (g > 148 * 16) g = 148 * 16;
-    prefill_pool_kernel<<<(unsigned)g, 256, 0, stream>>>(p);
+    if (p.fmt != kFmtBf16) {
+        prefill_store8_kernel<<<(unsigned)items, 256, 0, stream>>>(p);  // reads the head's logits
+    } else {
+        const int64_t rows = (int64_t)p.units * p.T;
+        int64_t g = (rows + 7) / 8;
+        if (g > 148 * 16) g = 148 * 16;
+        prefill_store_kernel<<<(unsigned)g, 256, 0, stream>>>(p);
+        g = (items + 7) / 8;
+        if (g > 148 * 16) g = 148 * 16;
+        prefill_pool_kernel<<<(unsigned)g, 256, 0, stream>>>(p);
+    }
     const size_t smem = (size_t)p.nblk * (sizeof(double) + 1);
     if (smem > 48 * 1024) {
         if (cudaFuncSetAttribute(prefill_gamma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

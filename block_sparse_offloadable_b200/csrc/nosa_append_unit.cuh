@@ -8,7 +8,7 @@
 // pre-exponential eviction score).
 #pragma once
 
-#include "nosa_internal.cuh"
+#include "nosa_kv8.cuh"
 
 namespace nosa {
 
@@ -54,6 +54,9 @@ __device__ __forceinline__ void gamma_e_worst(const int32_t *ge, int32_t ne, con
 // writes it once every CTA of the unit has read the old length), and fences the
 // device-side writes before the write-through to host memory, which no one
 // reads before a later kernel and which can be slow while PCIe is busy.
+// k8, the 8-bit store: the token's rows go to the unit's bf16 tail; the first token of a block codes the
+// block before it (the tail's content) into the store first.
+template <bool k8>
 __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, int lane, float e_tok,
                                             bool write_len = true) {
     const int32_t pos = p.seq_len[u];
@@ -64,6 +67,7 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
     const int32_t blk = pos >> 6, w = pos & 63;
     uint8_t *dst;
     uint8_t *host = nullptr;
+    uint8_t *coded = nullptr, *coded_host = nullptr;  // 8-bit store: the block coded by this call
     if (p.offload) {
         int32_t slot = -1;
         if (w == 0) {
@@ -79,6 +83,15 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
                 if (lane == 0) set_error(p.err, NOSA_EFLAG_NOSLOT);
                 return;
             }
+            if (k8 && blk >= 1) {
+                const int32_t sl = p.block_slot[(int64_t)u * p.nblk + blk - 1];
+                if (sl < 0) {
+                    if (lane == 0) set_error(p.err, NOSA_EFLAG_STATE);
+                    return;
+                }
+                coded = p.cache + ((int64_t)u * p.nslots + sl) * kBlock8Bytes;
+                coded_host = p.store + ((int64_t)u * p.nblk + blk - 1) * kBlock8Bytes;
+            }
             if (lane == 0) {
                 p.slot_block[(int64_t)u * p.nslots + slot] = blk;
                 p.block_slot[(int64_t)u * p.nblk + blk] = slot;
@@ -90,10 +103,18 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
                 return;
             }
         }
-        dst = p.cache + ((int64_t)u * p.nslots + slot) * kBlockBytes;
-        host = p.store + ((int64_t)u * p.nblk + blk) * kBlockBytes;
+        dst = k8 ? nullptr : p.cache + ((int64_t)u * p.nslots + slot) * kBlockBytes;
+        host = k8 ? nullptr : p.store + ((int64_t)u * p.nblk + blk) * kBlockBytes;
     } else {
-        dst = p.store + ((int64_t)u * p.nblk + blk) * kBlockBytes;
+        dst = k8 ? nullptr : p.store + ((int64_t)u * p.nblk + blk) * kBlockBytes;
+        if (k8 && w == 0 && blk >= 1) coded = p.store + ((int64_t)u * p.nblk + blk - 1) * kBlock8Bytes;
+    }
+    if (k8) {
+        dst = p.kv8.tail + (int64_t)u * kBlockBytes;
+        if (coded) {
+            code_tail(dst, coded, p.kv8.scales + (int64_t)u * p.kv8.scale_stride + blk - 1, lane, p.fmt);
+            __syncwarp();  // every lane has read the tail before its first rows are overwritten
+        }
     }
 
     // new key row (lanes 0-15) and value row (lanes 16-31), 16 B per lane
@@ -197,6 +218,11 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
     if (write_len && lane == 0) p.seq_len[u] = pos + 1;
     if (!write_len) __threadfence();  // the fused caller hands off to another CTA next
     if (host) *reinterpret_cast<uint4 *>(host + off) = val;  // write-through over PCIe, last
+    if (coded_host) {  // the codes each lane wrote above
+#pragma unroll 8
+        for (int i = lane; i < kBlock8Bytes / 8; i += 32)
+            reinterpret_cast<uint2 *>(coded_host)[i] = reinterpret_cast<const uint2 *>(coded)[i];
+    }
 }
 
 }  // namespace nosa

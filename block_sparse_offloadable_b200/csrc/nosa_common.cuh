@@ -7,6 +7,8 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -21,6 +23,9 @@ constexpr int kSubPerBlock = kBlock / kSub;   // 4
 constexpr int kRowBytes = kD * 2;             // one bf16 key or value row: 256 B
 constexpr int kHalfBlockBytes = kBlock * kRowBytes;  // keys (or values) of a block: 16 KiB
 constexpr int kBlockBytes = 2 * kHalfBlockBytes;     // keys + values of a block: 32 KiB
+constexpr int kRow8Bytes = kD;                // one 8-bit key or value row: 128 B
+constexpr int kHalfBlock8Bytes = kBlock * kRow8Bytes;  // keys (or values) of an 8-bit block: 8 KiB
+constexpr int kBlock8Bytes = 2 * kHalfBlock8Bytes;     // keys + values of an 8-bit block: 16 KiB
 constexpr int kMaxG = 8;                      // query heads per kv head handled by one tile
 constexpr int kMaxKq = 32;                    // Gamma_q fits one warp-wide sorted list
 constexpr int kMaxKe = 256;
@@ -138,6 +143,24 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// As above with f16 inputs.
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// D = A * B with f16 inputs.
+__device__ __forceinline__ void mma_16816_f16_zero(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+
 // Transpose an 8x8 bf16 matrix held one row-pair per lane (lane/4 = row).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -152,6 +175,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// The larger of two floats; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 // A 32-bit global load that stays where the program puts it (after the asm statements before it).
 __device__ __forceinline__ int32_t ld_volatile_s32(const int32_t *ptr) {

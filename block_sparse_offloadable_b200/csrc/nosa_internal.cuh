@@ -8,6 +8,18 @@
 
 namespace nosa {
 
+// How the blocks of a KV store are held (the NOSA_FLAG_KV_* bits).
+constexpr int kFmtBf16 = 0, kFmtInt8 = 1, kFmtE4m3 = 2;
+
+// The 8-bit store besides its blocks of codes, in device memory: the scales of each block's keys and
+// values, and the newest block of each unit in bf16.  A unit's row of scales is scale_stride blocks
+// (an even number: 16-byte aligned).
+struct Kv8 {
+    float2 *scales;        // [u][scale_stride] (s_K, s_V)
+    uint8_t *tail;         // [u][2][64][D] bf16
+    int32_t scale_stride;
+};
+
 struct AppendParams {
     const uint16_t *k_new;   // [u][T][D]
     const uint16_t *v_new;   // [u][T][D]
@@ -30,6 +42,8 @@ struct AppendParams {
     int32_t *pool;           // [u][nblk] fill reading: not-dropped candidates by E rank
     int32_t *pool_n;         // [u]
     int32_t nblk, nsub, nslots, units, heads_kv, k_e, offload, T, ck_bf16, fill;
+    int32_t fmt;             // kFmt*; not kFmtBf16: store and cache hold blocks of codes
+    Kv8 kv8;
 };
 
 struct SelectParams {
@@ -67,6 +81,24 @@ struct CacheParams {
     uint32_t *miss_list;      // [u][max_sel] workspace: (slot << 20 | block) of each block to fetch
     uint32_t *err;
     int32_t nblk, nslots, units, max_sel;
+    int32_t fmt;              // kFmt*: 32 or 16 KiB a block
+};
+
+struct EvictParams {
+    const float *weights;      // [u][nblk]
+    const int32_t *seq_len, *gamma_e, *gamma_n, *pool, *pool_n;  // pool: fill reading, else null
+    const uint8_t *store, *ck;
+    const float *e;
+    const double *blk_evict;
+    Kv8 kv8, dst_kv8;
+    int32_t *kept;             // [u][keep + 1] old numbers, ascending, -1 padded
+    float *dst_weights;        // [u][dst_nblk]
+    int32_t *dst_seq_len, *dst_gamma_e, *dst_gamma_n, *dst_pool, *dst_pool_n;
+    uint8_t *dst_store, *dst_ck;
+    float *dst_e;
+    double *dst_blk_evict;
+    int64_t max_ctx, dst_max_ctx;
+    int32_t nblk, dst_nblk, units, keep, sink, recent, k_e, fmt, ck_bf16;
 };
 
 // Work lists of the decode kernel.
@@ -100,8 +132,13 @@ struct DecodeParams {
     float *res_part;            // [u][kPartFloats] state over Gamma_e + local (written by resident, read by rest)
     uint32_t *res_bits;         // [u][bits_words] membership of Gamma_e + local (same)
     int32_t k_e, k_q, nblk, bits_words;
+    int32_t fmt;                // kFmt* of the blocks
+    Kv8 kv8;
+    float *weights;             // [u][nblk] or null: each attended block's weight is added
+    float *rec;                 // with weights: [items][4 warps][8 heads] log2 of each warp's sum of 2^x
 };
 
+constexpr int kRecFloats = 32;  // one item's weights
 constexpr int kPartFloats = 2 * kMaxG + kMaxG * kD;  // m[8], l[8], o[8][128]
 
 // The fused step (nosa_fused_step): append + select + sparse decode of a device-resident store in
@@ -128,7 +165,8 @@ struct StepParams {
 int launch_append(const AppendParams &p, cudaStream_t stream);
 int launch_select(const SelectParams &p, cudaStream_t stream);
 int launch_cache_sync(const CacheParams &p, cudaStream_t stream);
-int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, cudaStream_t stream);
+int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream);
+int launch_evict(const EvictParams &p, cudaStream_t stream);
 int launch_step(const StepParams &p, const CUtensorMap &tmap, cudaStream_t stream);
 
 // The argument checks of nosa_select (config, state, pointers, workspace), with

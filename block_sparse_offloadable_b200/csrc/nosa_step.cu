@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     if (warp == kSelectWarp) {
         // ---------------- selection warp ----------------
         if (cidx == 0) {
-            append_unit(sp.ap, u, lane, sp.ap.e_new[u], false);  // fences its writes
+            append_unit<false>(sp.ap, u, lane, sp.ap.e_new[u], false);  // fences its writes
             __syncwarp();
             if (lane == 0) st_release_gpu(sp.appended + u, 1);
         }

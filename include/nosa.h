@@ -13,7 +13,9 @@
  * nosa_compress_append_head (the eviction logits from the fused eviction head),
  * nosa_decode_resident + nosa_decode_rest (the attention split around the
  * select and the cache sync), nosa_dense_decode (the full-attention
- * comparator), nosa_select_noalloc, and the nosa_check_wait_timeout diagnostic.
+ * comparator), nosa_sparse_decode_weights and nosa_dense_decode_weights (the attention that also
+ * adds up the weight each block gets), nosa_evict (keep the blocks that got most),
+ * nosa_select_noalloc, and the nosa_check_wait_timeout diagnostic.
  *
  * Units.  A "unit" is one (sequence b, kv head g) pair, u = b * heads_kv + g.
  * Blocks are 64 tokens, sub-blocks 16 tokens; block j holds positions
@@ -106,11 +108,31 @@ typedef struct nosa_config {
 #define NOSA_FLAG_FILL 0x2
 
 /*
+ * The KV store in 8 bits: int8, or e4m3 (one of the two; 0x4 is not a flag).  The keys of a 64-token
+ * block share one fp32 scale, its values another: value = code * scale, with
+ *   a = max |x| over the 64 x 128 values, M = 127 (int8) or 448 (e4m3),
+ *   scale = fl32(a * fl32(1 / M)), r = fl32(fl32(1 / a) * M),
+ *   int8: code = x * r rounded once to the nearest integer, ties to even;
+ *   e4m3: code = fl32(x * r) rounded to the nearest e4m3, ties to even, saturating.
+ * a < 2^-100: scale 0, codes 0.  A value that is not finite: scale NaN, codes 0, so that attention
+ * over the block gives NaN.  The newest (local) block of a unit is held in bf16 in the unit's tail,
+ * and coded once, when the first token of the next block arrives.  Pooled keys and eviction scores
+ * are those of the bf16 input.  Every call works with these flags but nosa_fused_step
+ * (NOSA_ERR_UNSUPPORTED); a missed block is 16 KiB to fetch, not 32.
+ */
+#define NOSA_FLAG_KV_INT8 0x8
+#define NOSA_FLAG_KV_E4M3 0x10
+
+/*
  * Per-layer state.  Every buffer is caller-owned; nosa_state_bytes(cfg, NOSA_BUF_x)
  * gives its size.  Layouts (u = unit, nblk = max_ctx/64, nsub = max_ctx/16,
  * nslots = k_q + k_e + 2):
  *   kv_store    bf16 [u][nblk][2][64][D]; [..][0] = keys, [..][1] = values.
  *               Device memory if offload == 0, host memory if offload == 1.
+ *               With NOSA_FLAG_KV_INT8 / _E4M3: codes [u][nblk][2][64][D], one byte each, and,
+ *               in the same buffer where it is device memory (offload == 0), behind them (n2 = nblk
+ *               rounded up to an even number): scales fp32 [u][n2][2] (keys, values), padded
+ *               to a multiple of 256 bytes, then tails bf16 [u][2][64][D].
  *   evict_logit fp32 [u][max_ctx]   per-token eviction logit e_j (device)
  *   ck          fp32 [u][nsub][D]   compressed keys: mean of each 16-token sub-block (device);
  *               bf16 [u][nsub][D] with NOSA_FLAG_CK_BF16
@@ -120,6 +142,8 @@ typedef struct nosa_config {
  *   gamma_n     int32 [u]           |Gamma_e| (device)
  *   seq_len     int32 [u]           tokens held, L (device)
  *   cache       bf16 [u][nslots][2][64][D]  offload block cache (device; NULL if offload == 0)
+ *               with NOSA_FLAG_KV_INT8 / _E4M3: codes [u][nslots][2][64][D], then the scales
+ *               (of every block, resident or not) and tails as above
  *   slot_block  int32 [u][nslots]   block held by each cache slot, -1 = free (device; offload only)
  *   block_slot  int32 [u][nblk]     cache slot of each block, -1 = not resident (device; offload only)
  *   err         uint32 [1]          device error word (device)
@@ -167,7 +191,9 @@ enum nosa_call {
     NOSA_WS_DENSE_DECODE = 2,
     NOSA_WS_CACHE_SYNC = 3,
     NOSA_WS_SPLIT = 4,  /* the buffer nosa_decode_resident fills and nosa_decode_rest reads */
-    NOSA_WS_FUSED_STEP = 5
+    NOSA_WS_FUSED_STEP = 5,
+    NOSA_WS_SPARSE_WEIGHTS = 6,
+    NOSA_WS_DENSE_WEIGHTS = 7
 };
 
 /* Validate a configuration: NOSA_OK or a negative code. */
@@ -305,7 +331,7 @@ int nosa_append_select(const nosa_config *cfg, const nosa_state *st, const uint1
  * unit (it tags what the team's CTAs pass to one another), so after the
  * one-time zero fill it must serve only this state's nosa_fused_step calls.  NOSA_ERR_UNSUPPORTED with offload == 1 (the
  * cache sync runs between the selection and the decode) or NOSA_FLAG_FILL
- * (Gamma_e is formed after Gamma_q there).
+ * (Gamma_e is formed after Gamma_q there), and with an 8-bit KV store.
  */
 int nosa_fused_step(const nosa_config *cfg, const nosa_state *st, const uint16_t *k_new, const uint16_t *v_new,
                     const float *e_new, const uint16_t *q, int32_t *sel, int32_t *nsel, int32_t *gq, uint16_t *out,
@@ -361,6 +387,53 @@ int nosa_sparse_decode(const nosa_config *cfg, const nosa_state *st, const uint1
  */
 int nosa_dense_decode(const nosa_config *cfg, const nosa_state *st, const uint16_t *q,
                       uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * nosa_sparse_decode and nosa_dense_decode with the attention weight of every attended block added
+ * to a running total (any store format):
+ *
+ *   weights  device fp32 [u][nblk], in/out: weights[u][b] += sum over the G query heads of kv head g
+ *            and over the tokens j of block b of softmax_j(q_h . k_j * scale + e_j).  Blocks that
+ *            the call does not attend are left as they are.  Zero it when the sequences start.
+ *   ws       device workspace of nosa_workspace_bytes(cfg, NOSA_WS_SPARSE_WEIGHTS) or
+ *            (cfg, NOSA_WS_DENSE_WEIGHTS) bytes
+ *
+ * out as the plain calls write it.  Each block's total is one fp32 addition per call, in no
+ * order that varies (a block that sel names once; nosa_select's never repeat).  The dense form wants
+ * a device store, as nosa_dense_decode.
+ */
+int nosa_sparse_decode_weights(const nosa_config *cfg, const nosa_state *st, const uint16_t *q, const int32_t *sel,
+                               const int32_t *nsel, const int32_t *block_table, uint16_t *out, float *weights,
+                               void *ws, size_t ws_bytes, void *stream);
+int nosa_dense_decode_weights(const nosa_config *cfg, const nosa_state *st, const uint16_t *q, uint16_t *out,
+                              float *weights, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Eviction by accumulated attention weight (device store): the blocks of each unit that are kept,
+ * moved from state st into state dst, which may have another max_ctx -- a prompt's store into the
+ * smaller one that decoding uses, or a full store into a spare one.
+ *
+ *   weights      device fp32 [u][nblk]  e.g. from nosa_*_decode_weights; NaN counts as the largest
+ *   keep         candidates kept per unit; a unit with no more than that keeps all
+ *   sink, recent of these, the first `sink` and the last `recent` candidates are kept whatever
+ *                their weight (sink + recent <= keep)
+ *   dst_cfg, dst cfg with another max_ctx (> 64 * keep), scale as it likes: a state after
+ *                nosa_state_init, none of whose buffers overlaps st's; what it held is replaced
+ *   dst_weights  device fp32 [u][dst nblk] out: the kept blocks' weights, 0 elsewhere
+ *   kept         device int32 [u][keep + 1] out: the kept blocks' numbers in st, ascending (the local
+ *                block last), -1 padded; block i of dst was block kept[i]
+ *
+ * Of a unit's candidates: the protected ones, then those with the largest weight, ties to the lower
+ * block.  They keep their order, and the local block (always kept) stays the last.  Logits, pooled
+ * keys and eviction scores move with their block; members of Gamma_e (and, with NOSA_FLAG_FILL, of
+ * the pool) that are kept stay members, under their new numbers.  Buffer parts that no token of dst
+ * fills are left as they are.  NOSA_ERR_UNSUPPORTED with offload (there the block cache drops blocks
+ * by itself), NOSA_ERR_ARG if the configurations differ in more than max_ctx and scale or the
+ * states overlap, NOSA_ERR_CAPACITY if dst cannot hold keep + 1 blocks.
+ */
+int nosa_evict(const nosa_config *cfg, const nosa_state *st, const float *weights, int32_t keep, int32_t sink,
+               int32_t recent, const nosa_config *dst_cfg, const nosa_state *dst, float *dst_weights, int32_t *kept,
+               void *stream);
 
 /*
  * a5 split in two, so that the blocks already on the GPU are attended while
