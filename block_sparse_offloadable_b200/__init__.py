@@ -20,15 +20,16 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "_lib", "libnosa.so")
 _SOURCES = ["nosa_api.cu", "nosa_append.cu", "nosa_select.cu", "nosa_cache.cu", "nosa_decode.cu", "nosa_step.cu",
-            "nosa_noalloc.cu", "nosa_diag.cu", "nosa_evict.cu"]
+            "nosa_noalloc.cu", "nosa_diag.cu", "nosa_evict.cu", "nosa_decode_items.cu"]
 _HEADERS = ["nosa_common.cuh", "nosa_internal.cuh", "nosa_append_unit.cuh", "nosa_attend.cuh", "nosa_attend8.cuh",
-            "nosa_kv8.cuh"]
+            "nosa_kv8.cuh", "nosa_decode_work.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
 
 OK, ERR_ARG, ERR_CAPACITY, ERR_PTR, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED, ERR_DEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 EFLAG_CAPACITY, EFLAG_TIMEOUT, EFLAG_NOSLOT, EFLAG_STATE = 1, 2, 4, 8
 FLAG_CK_BF16, FLAG_FILL, FLAG_KV_INT8, FLAG_KV_E4M3 = 1, 2, 8, 16
+RECORD_BYTES = 16768  # 8-bit store: from one block's record to the next (codes, 64 logits, two scales, padding)
 KV_FORMATS = {"bf16": 0, "int8": FLAG_KV_INT8, "e4m3": FLAG_KV_E4M3}
 (BUF_KV_STORE, BUF_EVICT_LOGIT, BUF_CK, BUF_BLK_EVICT, BUF_GAMMA_E, BUF_GAMMA_N, BUF_SEQ_LEN, BUF_CACHE,
  BUF_SLOT_BLOCK, BUF_BLOCK_SLOT, BUF_ERR, BUF_POOL, BUF_POOL_N) = range(13)
@@ -404,20 +405,17 @@ class NosaLayer:
         return kept
 
     def kv8_views(self):
-        """An 8-bit layer's codes (int8 or float8_e4m3fn [units][blocks][2][64][D], device store; the cache's
-        [units][slots]... with offload), scales [units][blocks][2] and bf16 tails [units][2][64][D]."""
+        """Views of an 8-bit layer's buffer: codes (int8 or float8_e4m3fn [units][blocks][2][64][D]), scales fp32
+        [units][blocks][2] and bf16 tails [units][2][64][D].  With offload the blocks are the cache's slots."""
         cfg = self.cfg
         if not cfg.flags & (FLAG_KV_INT8 | FLAG_KV_E4M3):
             raise ValueError("kv8_views: the layer's KV store is bf16")
         buf = self.cache if cfg.offload else self.kv_store
-        nblk = cfg.max_ctx // cfg.block
-        held = cfg.k_q + cfg.k_e + 2 if cfg.offload else nblk
-        n2 = (nblk + 1) // 2 * 2
-        codes, scales = self.units * held * 2 * 64 * 128, self.units * n2 * 8
+        n = cfg.k_q + cfg.k_e + 2 if cfg.offload else cfg.max_ctx // cfg.block
         dtype = torch.int8 if cfg.flags & FLAG_KV_INT8 else torch.float8_e4m3fn
-        tail = codes + (scales + 255) // 256 * 256
-        return (buf[:codes].view(dtype).view(self.units, held, 2, 64, 128),
-                buf[codes:codes + scales].view(torch.float32).view(self.units, n2, 2)[:, :nblk],
+        r, tail = RECORD_BYTES, (self.units * n * RECORD_BYTES + 255) // 256 * 256
+        return (buf.view(dtype).as_strided((self.units, n, 2, 64, 128), (n * r, r, 8192, 128, 1)),
+                buf.view(torch.float32).as_strided((self.units, n, 2), (n * r // 4, r // 4, 1), 4096 + 64),
                 buf[tail:tail + self.units * 32768].view(torch.bfloat16).view(self.units, 2, 64, 128))
 
     def decode_step(self, k_new, v_new, e_new, q, out, stream=None):

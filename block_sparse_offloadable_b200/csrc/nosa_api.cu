@@ -33,7 +33,7 @@ int fmt_of(const nosa_config *c) {
     return (c->flags & NOSA_FLAG_KV_INT8) ? kFmtInt8 : (c->flags & NOSA_FLAG_KV_E4M3) ? kFmtE4m3 : kFmtBf16;
 }
 
-size_t block_bytes(const nosa_config *c) { return fmt_of(c) == kFmtBf16 ? kBlockBytes : kBlock8Bytes; }
+size_t block_bytes(const nosa_config *c) { return fmt_of(c) == kFmtBf16 ? kBlockBytes : kRec8Bytes; }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -76,30 +76,16 @@ int store_addr(const nosa_config *c, const nosa_state *st, uint8_t **out) {
     return NOSA_OK;
 }
 
-// The 8-bit store's scales and tails, behind the blocks of codes in the buffer that is in device memory
-// (kv_store, or the block cache with offload).  base may be null: the sizes alone.
-struct Kv8Region {
-    size_t scales, tail, total;
-};
-
-Kv8Region kv8_region(const nosa_config *c, const Geo &g) {
-    Kv8Region r;
-    const size_t u = (size_t)g.units;
-    r.scales = u * (size_t)(c->offload ? g.nslots : g.nblk) * kBlock8Bytes;
-    r.tail = r.scales + align256(u * (size_t)((g.nblk + 1) & ~1ll) * sizeof(float2));
-    r.total = r.tail + u * kBlockBytes;
-    return r;
+// The 8-bit store's tails lie behind the records in the buffer that is in device memory (kv_store, or
+// the block cache with offload): their offset, and the buffer's size.
+size_t tail_offset(const nosa_config *c, const Geo &g) {
+    return align256((size_t)g.units * (size_t)(c->offload ? g.nslots : g.nblk) * kRec8Bytes);
 }
+size_t with_tails(const nosa_config *c, const Geo &g) { return tail_offset(c, g) + (size_t)g.units * kBlockBytes; }
 
-Kv8 kv8_of(const nosa_config *c, const Geo &g, const nosa_state *st) {
-    Kv8 k = {};
-    if (fmt_of(c) == kFmtBf16) return k;
-    uint8_t *base = static_cast<uint8_t *>(c->offload ? st->cache : st->kv_store);
-    const Kv8Region r = kv8_region(c, g);
-    k.scales = reinterpret_cast<float2 *>(base + r.scales);
-    k.tail = base + r.tail;
-    k.scale_stride = (int32_t)((g.nblk + 1) & ~1ll);
-    return k;
+uint8_t *tail_of(const nosa_config *c, const Geo &g, const nosa_state *st) {
+    if (fmt_of(c) == kFmtBf16) return nullptr;
+    return static_cast<uint8_t *>(c->offload ? st->cache : st->kv_store) + tail_offset(c, g);
 }
 
 int check_state(const nosa_config *c, const nosa_state *st) {
@@ -134,19 +120,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Tensor map over a block-major KV buffer seen as [rows][128] rows of bf16 (box = 64 rows x 64 dims)
-// or of codes (64 rows x 128 dims): 128 bytes wide either way, 128-byte swizzle.
-int kv_tensor_map(CUtensorMap *map, const void *base, int64_t rows, int fmt = kFmtBf16) {
+// Tensor map over a block-major KV buffer seen as [rows][128] bf16 rows,
+// box = 64 rows x 64 dims (128 bytes), 128-byte swizzle.
+int kv_tensor_map(CUtensorMap *map, const void *base, int64_t rows) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return NOSA_ERR_CUDA;
-    const bool k8 = fmt != kFmtBf16;
     cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(k8 ? kRow8Bytes : kRowBytes)};
-    cuuint32_t box[2] = {k8 ? 128u : 64u, 64};
+    cuuint64_t strides[1] = {(cuuint64_t)kRowBytes};
+    cuuint32_t box[2] = {64, 64};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, k8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                     const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NOSA_OK : NOSA_ERR_CUDA;
+}
+
+// Tensor map over records of codes, [records][128 rows][128 bytes]: a box is one record's codes, the 64
+// key rows and the 64 value rows, 128-byte swizzle.
+int record_tensor_map(CUtensorMap *map, const void *base, int64_t records) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return NOSA_ERR_CUDA;
+    cuuint64_t dims[3] = {(cuuint64_t)kRow8Bytes, 2 * kBlock, (cuuint64_t)records};
+    cuuint64_t strides[2] = {(cuuint64_t)kRow8Bytes, (cuuint64_t)kRec8Bytes};
+    cuuint32_t box[3] = {kRow8Bytes, 2 * kBlock, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? NOSA_OK : NOSA_ERR_CUDA;
 }
@@ -259,15 +258,18 @@ int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, in
     }
     const int fmt = fmt_of(c);
     CUtensorMap map, tail_map;
-    if ((rc = kv_tensor_map(&map, base, g.units * bpu * 2 * kBlock, fmt))) return rc;
-    tail_map = map;
-    const Kv8 kv8 = kv8_of(c, g, st);
-    if (fmt != kFmtBf16 && (rc = kv_tensor_map(&tail_map, kv8.tail, g.units * 2 * kBlock))) return rc;
+    if (fmt == kFmtBf16) {
+        if ((rc = kv_tensor_map(&map, base, g.units * bpu * 2 * kBlock))) return rc;
+        tail_map = map;
+    } else {
+        if ((rc = record_tensor_map(&map, base, g.units * bpu))) return rc;
+        if ((rc = kv_tensor_map(&tail_map, tail_of(c, g, st), g.units * 2 * kBlock))) return rc;
+    }
 
     DecodeParams p;
     memset(&p, 0, sizeof(p));
     p.fmt = fmt;
-    p.kv8 = kv8;
+    p.records = static_cast<const uint8_t *>(base);
     p.nblk = (int32_t)g.nblk;
     if (weights) {
         p.weights = weights;
@@ -303,8 +305,10 @@ int run_decode(const nosa_config *c, const nosa_state *st, const uint16_t *q, in
     // streams one equal piece of one unit: a CTA then ends at most one partial state, at its end,
     // instead of stalling mid-stream on the hand-off of a unit it shares with its neighbour.
     if (mode == kModeSel && g.units <= decode_ctas())
-        p.pieces = (int32_t)std::min<int64_t>(decode_ctas() / g.units, g.max_sel);
-    return launch_decode(p, map, tail_map, static_cast<cudaStream_t>(stream));
+        p.pieces = (int32_t)std::min<int64_t>(decode_ctas() / g.units,
+                                              fmt != kFmtBf16 || weights ? (g.max_sel + 4) / 5 : g.max_sel);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return fmt != kFmtBf16 || weights ? launch_decode_items(p, map, tail_map, cs) : launch_decode(p, map, cs);
 }
 
 }  // namespace
@@ -337,7 +341,7 @@ size_t nosa_state_bytes(const nosa_config *c, int which) {
     const size_t u = (size_t)g.units;
     switch (which) {
     case NOSA_BUF_KV_STORE:
-        return fmt_of(c) != kFmtBf16 && !c->offload ? kv8_region(c, g).total : u * g.nblk * block_bytes(c);
+        return fmt_of(c) != kFmtBf16 && !c->offload ? with_tails(c, g) : u * g.nblk * block_bytes(c);
     case NOSA_BUF_EVICT_LOGIT: return u * c->max_ctx * sizeof(float);
     case NOSA_BUF_CK: return u * g.nsub * kD * ((c->flags & NOSA_FLAG_CK_BF16) ? 2 : sizeof(float));
     case NOSA_BUF_BLK_EVICT: return u * g.nblk * sizeof(double);
@@ -346,7 +350,7 @@ size_t nosa_state_bytes(const nosa_config *c, int which) {
     case NOSA_BUF_SEQ_LEN: return u * sizeof(int32_t);
     case NOSA_BUF_CACHE:
         if (!c->offload) return 0;
-        return fmt_of(c) != kFmtBf16 ? kv8_region(c, g).total : u * g.nslots * kBlockBytes;
+        return fmt_of(c) != kFmtBf16 ? with_tails(c, g) : u * g.nslots * kBlockBytes;
     case NOSA_BUF_SLOT_BLOCK: return c->offload ? u * g.nslots * sizeof(int32_t) : 0;
     case NOSA_BUF_BLOCK_SLOT: return c->offload ? u * g.nblk * sizeof(int32_t) : 0;
     case NOSA_BUF_ERR: return sizeof(uint32_t);
@@ -419,7 +423,7 @@ int make_append(const nosa_config *c, const nosa_state *st, const uint16_t *k_ne
     p.fill = (c->flags & NOSA_FLAG_FILL) != 0;
     p.pool = p.fill ? st->pool : nullptr; p.pool_n = p.fill ? st->pool_n : nullptr;
     p.fmt = fmt_of(c);
-    p.kv8 = kv8_of(c, g, st);
+    p.tail = tail_of(c, g, st);
     *out = p;
     return NOSA_OK;
 }
@@ -670,7 +674,7 @@ int nosa_evict(const nosa_config *c, const nosa_state *st, const float *weights,
     p.weights = weights;
     p.seq_len = st->seq_len; p.gamma_e = st->gamma_e; p.gamma_n = st->gamma_n;
     p.store = s; p.ck = static_cast<const uint8_t *>(st->ck); p.e = st->evict_logit; p.blk_evict = st->blk_evict;
-    p.kv8 = kv8_of(c, g, st); p.dst_kv8 = kv8_of(dc, dg, dst);
+    p.tail = tail_of(c, g, st); p.dst_tail = tail_of(dc, dg, dst);
     p.kept = kept;
     p.dst_weights = dst_weights;
     p.dst_seq_len = dst->seq_len; p.dst_gamma_e = dst->gamma_e; p.dst_gamma_n = dst->gamma_n;

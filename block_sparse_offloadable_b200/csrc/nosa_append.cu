@@ -160,9 +160,9 @@ __global__ void __launch_bounds__(256) prefill_pool_kernel(const AppendParams p)
 }
 
 // A block's rows (bf16, in the registers of a CTA of 256 threads: thread's piece i is piece
-// tid + 256 i of the keys and of the values) to codes at dst; returns the scales.  Two barriers.
-__device__ __forceinline__ float2 code_block(const uint4 (&k)[4], const uint4 (&v)[4], uint8_t *dst,
-                                             uint32_t (*s_max)[8], int fmt) {
+// tid + 256 i of the keys and of the values; e: its logits) to the record dst.  Two barriers.
+__device__ __forceinline__ void code_block(const uint4 (&k)[4], const uint4 (&v)[4], const float *e, uint8_t *dst,
+                                           uint32_t (*s_max)[8], int fmt) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t ak = 0, av = 0;
 #pragma unroll
@@ -190,7 +190,9 @@ __device__ __forceinline__ float2 code_block(const uint4 (&k)[4], const uint4 (&
         to[256 * i] = code8(k[i], sk.y, fmt);
         to[kHalfBlock8Bytes / 8 + 256 * i] = code8(v[i], sv.y, fmt);
     }
-    return make_float2(sk.x, sv.x);
+    float *side = reinterpret_cast<float *>(dst + kBlock8Bytes);
+    if (tid < kBlock) side[tid] = e[tid];
+    else if (tid < kBlock + 2) side[tid] = tid == kBlock ? sk.x : sv.x;
 }
 
 // The same two steps for the 8-bit store, in one pass over the input: one CTA per block stages its
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(256) prefill_store8_kernel(const AppendParams 
     for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(ks)[tid + 256 * i] = k[i];
     __syncthreads();
     if (local) {
-        uint4 *tail = reinterpret_cast<uint4 *>(p.kv8.tail + (int64_t)u * kBlockBytes);
+        uint4 *tail = reinterpret_cast<uint4 *>(p.tail + (int64_t)u * kBlockBytes);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if ((tid >> 4) + 16 * i < rows) {
@@ -238,8 +240,7 @@ __global__ void __launch_bounds__(256) prefill_store8_kernel(const AppendParams 
                 tail[kHalfBlockBytes / 16 + tid + 256 * i] = v[i];
             }
     } else {
-        const float2 sc = code_block(k, v, p.store + ((int64_t)u * p.nblk + blk) * kBlock8Bytes, s_max, p.fmt);
-        if (tid == 0) p.kv8.scales[(int64_t)u * p.kv8.scale_stride + blk] = sc;
+        code_block(k, v, s_e, p.store + ((int64_t)u * p.nblk + blk) * kRec8Bytes, s_max, p.fmt);
     }
     // pooled keys: thread = (sub-block, pair of dims)
     const int sub = tid >> 6, pair = tid & 63;
@@ -431,7 +432,8 @@ __global__ void __launch_bounds__(256) prefill_gamma_kernel(const AppendParams p
                     k[i] = K[256 * i];
                     v[i] = V[256 * i];
                 }
-                code_block(k, v, p.cache + ((int64_t)u * p.nslots + 1 + j) * kBlock8Bytes, s_max, p.fmt);
+                code_block(k, v, p.e_store + (int64_t)u * p.max_ctx + (int64_t)ge[j] * kBlock,
+                           p.cache + ((int64_t)u * p.nslots + 1 + j) * kRec8Bytes, s_max, p.fmt);
             }
             return;
         }

@@ -89,8 +89,8 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
                     if (lane == 0) set_error(p.err, NOSA_EFLAG_STATE);
                     return;
                 }
-                coded = p.cache + ((int64_t)u * p.nslots + sl) * kBlock8Bytes;
-                coded_host = p.store + ((int64_t)u * p.nblk + blk - 1) * kBlock8Bytes;
+                coded = p.cache + ((int64_t)u * p.nslots + sl) * kRec8Bytes;
+                coded_host = p.store + ((int64_t)u * p.nblk + blk - 1) * kRec8Bytes;
             }
             if (lane == 0) {
                 p.slot_block[(int64_t)u * p.nslots + slot] = blk;
@@ -107,12 +107,12 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
         host = k8 ? nullptr : p.store + ((int64_t)u * p.nblk + blk) * kBlockBytes;
     } else {
         dst = k8 ? nullptr : p.store + ((int64_t)u * p.nblk + blk) * kBlockBytes;
-        if (k8 && w == 0 && blk >= 1) coded = p.store + ((int64_t)u * p.nblk + blk - 1) * kBlock8Bytes;
+        if (k8 && w == 0 && blk >= 1) coded = p.store + ((int64_t)u * p.nblk + blk - 1) * kRec8Bytes;
     }
     if (k8) {
-        dst = p.kv8.tail + (int64_t)u * kBlockBytes;
+        dst = p.tail + (int64_t)u * kBlockBytes;
         if (coded) {
-            code_tail(dst, coded, p.kv8.scales + (int64_t)u * p.kv8.scale_stride + blk - 1, lane, p.fmt);
+            code_tail(dst, p.e_store + (int64_t)u * p.max_ctx + (int64_t)(blk - 1) * kBlock, coded, lane, p.fmt);
             __syncwarp();  // every lane has read the tail before its first rows are overwritten
         }
     }
@@ -218,10 +218,11 @@ __device__ __forceinline__ void append_unit(const AppendParams &p, int32_t u, in
     if (write_len && lane == 0) p.seq_len[u] = pos + 1;
     if (!write_len) __threadfence();  // the fused caller hands off to another CTA next
     if (host) *reinterpret_cast<uint4 *>(host + off) = val;  // write-through over PCIe, last
-    if (coded_host) {  // the codes each lane wrote above
+    if (coded_host) {  // the record that this warp wrote above
+        __syncwarp();
 #pragma unroll 8
-        for (int i = lane; i < kBlock8Bytes / 8; i += 32)
-            reinterpret_cast<uint2 *>(coded_host)[i] = reinterpret_cast<const uint2 *>(coded)[i];
+        for (int i = lane; i < kHeld8Bytes / 16; i += 32)
+            reinterpret_cast<uint4 *>(coded_host)[i] = reinterpret_cast<const uint4 *>(coded)[i];
     }
 }
 

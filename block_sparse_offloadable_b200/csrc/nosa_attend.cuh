@@ -16,8 +16,6 @@
 // in a merge of their partial (m, l, o) records by the last one to finish.
 #pragma once
 
-#include <type_traits>
-
 #include "nosa_internal.cuh"
 
 namespace nosa {
@@ -44,8 +42,9 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
     return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
+template <int kThreads = kConsThreads>
 __device__ __forceinline__ void consumer_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsThreads) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
@@ -69,54 +68,12 @@ struct WarpState {
     }
 };
 
-// An eviction logit in the log2 domain.  The lowest finite floats would become -inf, which masks a
-// token outright: they stay finite, so that a row in which every token has such a mask is their mean.
-__device__ __forceinline__ float bias_log2(float e) {
-    constexpr float kLow = -2.3e38f;  // times log2(e): above the lowest float
-    return (e < kLow && e != kNegInf ? kLow : e) * kLog2e;
-}
-
-// The dims of a lane's accumulators: o[t][0..1] hold dim psi(t, sig) of heads 2c, 2c+1 and
-// o[t][2..3] dim psi(t, sig) + 1; at() places a dim in the merge scratch so that a warp's stores of
-// one t hit 32 distinct banks.
-struct DimsBf16 {  // two 16-byte chunks of a 256-byte row, one in each 128-byte half
-    static __device__ __forceinline__ int psi(int t, int sig) { return 64 * (t >> 2) + 8 * sig + 2 * (t & 3); }
-    static __device__ __forceinline__ int at(int x) { return swz(x); }
-};
-struct Dims8 {  // one 16-byte chunk of a 128-byte row
-    static __device__ __forceinline__ int psi(int t, int sig) { return 16 * sig + 2 * t; }
-    static __device__ __forceinline__ int at(int x) { return x ^ ((x >> 5) & 1) ^ (((x >> 6) & 1) << 3); }
-};
-
-// Leave the weight of this warp's 16 tokens, per head, for the unit's last CTA: the log2 of the sum
-// of 2^x over the tokens (s0, s1: this lane's sums relative to m0, m1; -inf where nothing is seen).
-// rec: the item's 32 values, [4 warps][8 heads].
-__device__ __forceinline__ void leave_weights(float *rec, float s0, float s1, float m0, float m1, int warp, int r,
-                                              int c) {
-#pragma unroll
-    for (int sh = 4; sh < 32; sh <<= 1) {
-        s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, sh);
-        s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, sh);
-    }
-    if (r == 0)
-        *reinterpret_cast<float2 *>(rec + warp * kMaxG + 2 * c) = make_float2(m0 + log2f(s0), m1 + log2f(s1));
-}
-
-// The item has nothing to attend: its weights are zero.
-__device__ __forceinline__ void leave_none(float *rec, int warp, int r, int c) {
-    if (r == 0) *reinterpret_cast<float2 *>(rec + warp * kMaxG + 2 * c) = make_float2(kNegInf, kNegInf);
-}
-
-// Attention of this warp's 16 tokens of one staged bf16 block.  kWeights: leave their weights in rec.
-// Dims: where the output dims of a lane lie (DimsBf16, or Dims8 for the bf16 tail of an 8-bit store:
-// its value loads then have a two-way bank conflict, on one block of a unit).
-template <class Dims = DimsBf16, bool kWeights = false>
+// Attention of this warp's 16 tokens of one staged block.
 __device__ __forceinline__ void attend_block(WarpState &st, const uint32_t (&qf)[8][2], const uint8_t *t,
                                              const float *eb, int32_t lb, int32_t L, float qk_log2,
-                                             int warp, int c, int sig, float *rec = nullptr, int r = 0) {
+                                             int warp, int c, int sig) {
     const int rowA = warp * 16 + sig, rowB = rowA + 8;   // key rows of C rows r, r+8
     const int vt0 = warp * 16 + c;                        // value rows of k = 2c, 2c+1, 2c+8, 2c+9
-    constexpr bool kWide = std::is_same<Dims, Dims8>::value;  // chunks 2 sig, 2 sig + 1 of the row
     const int off0 = ((sig ^ c) << 4), off1 = ((sig ^ (c + 4)) << 4);
     // ---- S^T (16 tokens x 8 heads) = K Q^T, two independent accumulation chains ----
     float sacc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -136,22 +93,18 @@ __device__ __forceinline__ void attend_block(WarpState &st, const uint32_t (&qf)
     for (int x = 0; x < 4; ++x) sacc[x] += sacc2[x];
     // ---- online softmax over the 16 tokens, per head (2c, 2c+1) ----
     const int64_t posA = (int64_t)lb * kBlock + rowA, posB = posA + 8;
-    constexpr bool kLowest = kWide || kWeights;
-    const float eA = kLowest ? bias_log2(eb[rowA]) : eb[rowA] * kLog2e;
-    const float eB = kLowest ? bias_log2(eb[rowB]) : eb[rowB] * kLog2e;
+    const float eA = eb[rowA] * kLog2e, eB = eb[rowB] * kLog2e;
     const float x0 = posA < L ? fmaf(sacc[0], qk_log2, eA) : kNegInf;
     const float x1 = posA < L ? fmaf(sacc[1], qk_log2, eA) : kNegInf;
     const float x2 = posB < L ? fmaf(sacc[2], qk_log2, eB) : kNegInf;
     const float x3 = posB < L ? fmaf(sacc[3], qk_log2, eB) : kNegInf;
-    // the 8-bit store's states carry NaN on, as attend8 does
-    const auto row_max = [](float a, float b) { return kWide ? max_nan(a, b) : fmaxf(a, b); };
-    float bm0 = row_max(x0, x2), bm1 = row_max(x1, x3);
+    float bm0 = fmaxf(x0, x2), bm1 = fmaxf(x1, x3);
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) {
-        bm0 = row_max(bm0, __shfl_xor_sync(0xFFFFFFFFu, bm0, sh));
-        bm1 = row_max(bm1, __shfl_xor_sync(0xFFFFFFFFu, bm1, sh));
+        bm0 = fmaxf(bm0, __shfl_xor_sync(0xFFFFFFFFu, bm0, sh));
+        bm1 = fmaxf(bm1, __shfl_xor_sync(0xFFFFFFFFu, bm1, sh));
     }
-    const float mn0 = row_max(st.m0, bm0), mn1 = row_max(st.m1, bm1);
+    const float mn0 = fmaxf(st.m0, bm0), mn1 = fmaxf(st.m1, bm1);
     const float c0 = (mn0 == kNegInf) ? 1.f : exp2f(st.m0 - mn0);
     const float c1 = (mn1 == kNegInf) ? 1.f : exp2f(st.m1 - mn1);
     const float p0 = (mn0 == kNegInf) ? 0.f : exp2f(x0 - mn0);
@@ -160,13 +113,9 @@ __device__ __forceinline__ void attend_block(WarpState &st, const uint32_t (&qf)
     const float p3 = (mn1 == kNegInf) ? 0.f : exp2f(x3 - mn1);
     st.m0 = mn0;
     st.m1 = mn1;
-    if constexpr (kWeights)
-        leave_weights(rec, p0 + p2, p1 + p3, mn0 == kNegInf ? 0.f : mn0, mn1 == kNegInf ? 0.f : mn1, warp, r, c);
     const uint32_t plo = pack_bf16x2(p0, p1), phi = pack_bf16x2(p2, p3);
-    // the denominator sums what the numerator sums; the weights want it without P's rounding (which
-    // is unbiased: out moves by less than its own last bit)
-    st.l0 = fmaf(st.l0, c0, kWeights ? p0 + p2 : bf16_lo(plo) + bf16_lo(phi));
-    st.l1 = fmaf(st.l1, c1, kWeights ? p1 + p3 : bf16_hi(plo) + bf16_hi(phi));
+    st.l0 = fmaf(st.l0, c0, bf16_lo(plo) + bf16_lo(phi));
+    st.l1 = fmaf(st.l1, c1, bf16_hi(plo) + bf16_hi(phi));
 #pragma unroll
     for (int tt = 0; tt < 8; ++tt) {
         st.o[tt][0] *= c0; st.o[tt][1] *= c1;
@@ -177,13 +126,11 @@ __device__ __forceinline__ void attend_block(WarpState &st, const uint32_t (&qf)
     const bool partial = (int64_t)lb * kBlock + kBlock > L;
 #pragma unroll
     for (int bx = 0; bx < 2; ++bx) {
-        const uint8_t *vb = t + (2 + (kWide ? sig >> 2 : bx)) * kBoxBytes;
-        const int o0 = kWide ? ((2 * (sig & 3) + bx) ^ c) << 4 : off0;
-        const int o1 = kWide ? ((2 * (sig & 3) + bx) ^ (c + 4)) << 4 : off1;
-        uint4 v0 = lds128(vb + (vt0 + 0) * 128 + o0);
-        uint4 v1 = lds128(vb + (vt0 + 4) * 128 + o1);
-        uint4 v2 = lds128(vb + (vt0 + 8) * 128 + o0);
-        uint4 v3 = lds128(vb + (vt0 + 12) * 128 + o1);
+        const uint8_t *vb = t + (2 + bx) * kBoxBytes;
+        uint4 v0 = lds128(vb + (vt0 + 0) * 128 + off0);
+        uint4 v1 = lds128(vb + (vt0 + 4) * 128 + off1);
+        uint4 v2 = lds128(vb + (vt0 + 8) * 128 + off0);
+        uint4 v3 = lds128(vb + (vt0 + 12) * 128 + off1);
         if (partial) {  // rows at or beyond L hold stale bits: keep them out of 0 * x
             const int64_t b0 = (int64_t)lb * kBlock + vt0;
             const uint4 z = make_uint4(0, 0, 0, 0);
@@ -212,7 +159,6 @@ __device__ __forceinline__ void store_bf16(uint16_t *dst, float v) {
 // Segment end, first half: group 0 folds its per-lane states into group 1's, lane by lane, and
 // each warp of group 1 leaves the folded (m, l, o) of its 16-token slice in its scratch slot
 // (padded, swizzled layout).  Called by every consumer thread; two consumer barriers inside.
-template <class Dims = DimsBf16>
 __device__ __forceinline__ void fold_groups(const WarpState &st, float *scratch, int grp, int wq, int r, int c,
                                             int sig) {
     float l0 = st.l0, l1 = st.l1;
@@ -230,11 +176,11 @@ __device__ __forceinline__ void fold_groups(const WarpState &st, float *scratch,
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const int psi = Dims::psi(t, sig);
-            oo[(2 * c) * kHS + Dims::at(psi)] = st.o[t][0];
-            oo[(2 * c + 1) * kHS + Dims::at(psi)] = st.o[t][1];
-            oo[(2 * c) * kHS + Dims::at(psi + 1)] = st.o[t][2];
-            oo[(2 * c + 1) * kHS + Dims::at(psi + 1)] = st.o[t][3];
+            const int psi = 64 * (t >> 2) + 8 * sig + 2 * (t & 3);
+            oo[(2 * c) * kHS + swz(psi)] = st.o[t][0];
+            oo[(2 * c + 1) * kHS + swz(psi)] = st.o[t][1];
+            oo[(2 * c) * kHS + swz(psi + 1)] = st.o[t][2];
+            oo[(2 * c + 1) * kHS + swz(psi + 1)] = st.o[t][3];
         }
     }
     consumer_sync();
@@ -249,11 +195,11 @@ __device__ __forceinline__ void fold_groups(const WarpState &st, float *scratch,
         float om[8][4];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const int psi = Dims::psi(t, sig);
-            om[t][0] = fmaf(fa0, oo[(2 * c) * kHS + Dims::at(psi)], fb0 * st.o[t][0]);
-            om[t][1] = fmaf(fa1, oo[(2 * c + 1) * kHS + Dims::at(psi)], fb1 * st.o[t][1]);
-            om[t][2] = fmaf(fa0, oo[(2 * c) * kHS + Dims::at(psi + 1)], fb0 * st.o[t][2]);
-            om[t][3] = fmaf(fa1, oo[(2 * c + 1) * kHS + Dims::at(psi + 1)], fb1 * st.o[t][3]);
+            const int psi = 64 * (t >> 2) + 8 * sig + 2 * (t & 3);
+            om[t][0] = fmaf(fa0, oo[(2 * c) * kHS + swz(psi)], fb0 * st.o[t][0]);
+            om[t][1] = fmaf(fa1, oo[(2 * c + 1) * kHS + swz(psi)], fb1 * st.o[t][1]);
+            om[t][2] = fmaf(fa0, oo[(2 * c) * kHS + swz(psi + 1)], fb0 * st.o[t][2]);
+            om[t][3] = fmaf(fa1, oo[(2 * c + 1) * kHS + swz(psi + 1)], fb1 * st.o[t][3]);
         }
         __syncwarp();  // every lane has read m, l before lanes r == 0 overwrite them
         if (r == 0) {
@@ -263,11 +209,11 @@ __device__ __forceinline__ void fold_groups(const WarpState &st, float *scratch,
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const int psi = Dims::psi(t, sig);
-            oo[(2 * c) * kHS + Dims::at(psi)] = om[t][0];
-            oo[(2 * c + 1) * kHS + Dims::at(psi)] = om[t][1];
-            oo[(2 * c) * kHS + Dims::at(psi + 1)] = om[t][2];
-            oo[(2 * c + 1) * kHS + Dims::at(psi + 1)] = om[t][3];
+            const int psi = 64 * (t >> 2) + 8 * sig + 2 * (t & 3);
+            oo[(2 * c) * kHS + swz(psi)] = om[t][0];
+            oo[(2 * c + 1) * kHS + swz(psi)] = om[t][1];
+            oo[(2 * c) * kHS + swz(psi + 1)] = om[t][2];
+            oo[(2 * c + 1) * kHS + swz(psi + 1)] = om[t][3];
         }
     }
     consumer_sync();
@@ -275,7 +221,6 @@ __device__ __forceinline__ void fold_groups(const WarpState &st, float *scratch,
 
 // Segment end, second half, for head h and dim d: the four warps' slices merged into (M, acc, lsum),
 // the state of the whole segment (acc / lsum is its output).
-template <class Dims = DimsBf16>
 __device__ __forceinline__ void merged_state(const float *scratch, int h, int d, float &M, float &acc, float &lsum) {
     M = kNegInf;
 #pragma unroll
@@ -286,7 +231,7 @@ __device__ __forceinline__ void merged_state(const float *scratch, int h, int d,
     for (int w = 0; w < kDecW; ++w) {
         const float mw = scratch[w * kScr + h];
         const float f = (mw == kNegInf) ? 0.f : exp2f(mw - M);
-        acc = fmaf(f, scratch[w * kScr + 2 * kMaxG + h * kHS + Dims::at(d)], acc);
+        acc = fmaf(f, scratch[w * kScr + 2 * kMaxG + h * kHS + swz(d)], acc);
         lsum = fmaf(f, scratch[w * kScr + kMaxG + h], lsum);
     }
 }
@@ -322,11 +267,11 @@ __device__ __forceinline__ uint2 pack_out4(float4 acc, float ls) {
 // src0 + t * stride, in piece order, in one pass: each consumer thread takes 4 dims of one head
 // and issues its loads at once (all of them with at most kAtOnce pieces: one round trip; more
 // registers).  Writes bf16 out, and where s_lse is given the log2 of each head's whole sum there.
-template <int kAtOnce = kFewPieces, bool kNan = false>
+template <int kAtOnce = kFewPieces, bool kNan = false, int kThreads = kConsThreads>
 __device__ __forceinline__ void merge_pieces_onepass(const float *src0, int64_t stride, int C, int G, uint16_t *out,
                                                      int ctid, float *s_lse = nullptr) {
     static_assert(kAtOnce <= kOnePassPieces, "at most kOnePassPieces pieces");
-    for (int v = ctid; v < G * (kD / 4); v += kConsThreads) {
+    for (int v = ctid; v < G * (kD / 4); v += kThreads) {
         const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
         float mt[kOnePassPieces];
         float ls = 0.f, M = kNegInf;
@@ -397,10 +342,10 @@ __device__ __forceinline__ MergeScratch merge_scratch(float *scratch, int nc) {
 
 // kNan as in has_weight.  One warp per head finds the weights, then each consumer thread combines 4 dims of one head.
 // res == nullptr: writes the bf16 output; otherwise the merged record (the split decode's state).
-template <bool kNan = false>
+template <bool kNan = false, int kThreads = kConsThreads>
 __device__ __forceinline__ void merge_general(const MergeScratch &ms, int nc, int G, uint16_t *out, float *res,
                                              int warp, int lane, int ctid) {
-    for (int h = warp; h < G; h += kConsWarps) {
+    for (int h = warp; h < G; h += kThreads / 32) {
         float M = kNegInf;
         for (int t = lane; t < nc; t += 32) M = fmaxf(M, __ldcg(ms.src[t] + h));
 #pragma unroll
@@ -419,8 +364,8 @@ __device__ __forceinline__ void merge_general(const MergeScratch &ms, int nc, in
             ms.Ms[h] = M;
         }
     }
-    consumer_sync();
-    for (int v = ctid; v < G * (kD / 4); v += kConsThreads) {  // 4 dims per thread
+    consumer_sync<kThreads>();
+    for (int v = ctid; v < G * (kD / 4); v += kThreads) {  // 4 dims per thread
         const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4

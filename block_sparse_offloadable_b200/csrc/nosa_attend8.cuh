@@ -14,15 +14,54 @@
 // normal one 2^-28 of it: a token loses bits only below that, and is lost only below 2^-39 of the
 // largest (2^20 tokens of that size are 2^-19 of the sum).
 //
-// Layout.  As attend_block: warp w of a group owns tokens 16w..16w+15, S^T = C Q^T and
-// O^T += C'^T P^T in m16n8k16 tiles.  One 16-byte shared load holds 16 dims of a row (half as many
-// loads as bf16); the codes become f16 pairs in registers: int8 by placing the byte under the
-// exponent of 1024 (one permute) and subtracting 1152, e4m3 by the conversion instruction.
+// Layout.  One warp attends a whole block of 64 tokens, in four m16n8k16 slices of S^T = C Q^T and
+// O^T += C'^T P^T (attend_block gives a block to four warps): the maximum, its two reductions over
+// lanes, the rescaling and the scale of the values are paid once per block, and the four slices keep
+// the matrix instructions' latency covered.  One 16-byte shared load holds 16 dims of a row; the
+// codes become f16 pairs in registers: int8 by placing the byte under the exponent of 1024 (one
+// permute) and subtracting 1152, e4m3 by the conversion instruction.
 #pragma once
+
+#include <type_traits>
 
 #include "nosa_attend.cuh"
 
 namespace nosa {
+
+// An eviction logit in the log2 domain.  The lowest finite floats would become -inf, which masks a
+// token outright: they stay finite, so that a row in which every token has such a mask is their mean.
+__device__ __forceinline__ float bias_log2(float e) {
+    constexpr float kLow = -2.3e38f;  // times log2(e): above the lowest float
+    return (e < kLow && e != kNegInf ? kLow : e) * kLog2e;
+}
+
+// The dims of a lane's accumulators: o[t][0..1] hold dim psi(t, sig) of heads 2c, 2c+1 and
+// o[t][2..3] dim psi(t, sig) + 1; at() places a dim in the merge scratch so that a warp's stores of
+// one t hit 32 distinct banks.
+struct DimsBf16 {  // two 16-byte chunks of a 256-byte row, one in each 128-byte half
+    static __device__ __forceinline__ int psi(int t, int sig) { return 64 * (t >> 2) + 8 * sig + 2 * (t & 3); }
+    static __device__ __forceinline__ int at(int x) { return swz(x); }
+};
+struct Dims8 {  // one 16-byte chunk of a 128-byte row
+    static __device__ __forceinline__ int psi(int t, int sig) { return 16 * sig + 2 * t; }
+    static __device__ __forceinline__ int at(int x) { return x ^ ((x >> 5) & 1) ^ (((x >> 6) & 1) << 3); }
+};
+
+// Leave an item's weights, per head, for the unit's last CTA: the log2 of the sum of 2^x over its
+// tokens (s0, s1: this lane's sums relative to m0, m1; -inf where nothing is seen).  rec: 8 values.
+__device__ __forceinline__ void leave_weights(float *rec, float s0, float s1, float m0, float m1, int r, int c) {
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1) {
+        s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, sh);
+        s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, sh);
+    }
+    if (r == 0) *reinterpret_cast<float2 *>(rec + 2 * c) = make_float2(m0 + log2f(s0), m1 + log2f(s1));
+}
+
+// The item has nothing to attend: its weights are zero.
+__device__ __forceinline__ void leave_none(float *rec, int r, int c) {
+    if (r == 0) *reinterpret_cast<float2 *>(rec + 2 * c) = make_float2(kNegInf, kNegInf);
+}
 
 // The two low (two high) codes of a word as an f16 pair.  int8 codes come biased: c ^ 0x80.
 template <int kFmt>
@@ -91,49 +130,53 @@ __device__ __forceinline__ void load_query8(Query8 &Q, const uint16_t *q, int G,
 
 constexpr float kPBias = 14.f;  // m is the running maximum less this
 
-// One block of codes (t: 64 key rows, then 64 value rows, 128 bytes each, 128-byte swizzle), every
-// token of it before the newest block.  sK, sV: its scales.  kWeights: as attend_block.
-template <int kFmt, bool kWeights>
-__device__ __forceinline__ void attend8(WarpState &st, const Query8 &Q, const uint8_t *t, const float *eb, float sK,
-                                        float sV, float qk_log2, int warp, int r, int c, int sig, float *rec) {
-    const int rowA = warp * 16 + sig, rowB = rowA + 8;
-    // ---- S^T (16 tokens x 8 heads), two independent accumulation chains ----
-    float sacc[4] = {0.f, 0.f, 0.f, 0.f};
-    float sacc2[4] = {0.f, 0.f, 0.f, 0.f};
+// The softmax step of one block in a warp: x[i] holds slice i's logits (rows r and r + 8 of the slice,
+// heads 2c and 2c + 1) in the log2 domain.  Updates m and l, rescales o, leaves P in p.  kNan: NaN is
+// carried on; else it is passed over, as attend_block does.  bias: m is the maximum less this.
+template <bool kNan, bool kWeights, bool kF16>
+__device__ __forceinline__ void softmax_step(WarpState &st, float (&x)[4][4], uint32_t (&pb)[4][2], float bias, int r,
+                                             int c, float *rec) {
+    const auto row_max = [](float a, float b) { return kNan ? max_nan(a, b) : fmaxf(a, b); };
+    float bm0 = row_max(x[0][0], x[0][2]), bm1 = row_max(x[0][1], x[0][3]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int off = (((c + 4 * j) ^ sig) << 4);
-        const uint4 ka = lds128(t + rowA * kRow8Bytes + off);
-        const uint4 kb = lds128(t + rowB * kRow8Bytes + off);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t x = biased<kFmt>(word(ka, w)), y = biased<kFmt>(word(kb, w));
-            const uint32_t a[4] = {codes_lo<kFmt>(x), codes_lo<kFmt>(y), codes_hi<kFmt>(x), codes_hi<kFmt>(y)};
-            mma_16816_f16((w & 1) ? sacc2 : sacc, a, Q.f[4 * j + w]);
-        }
+    for (int i = 1; i < 4; ++i) {
+        bm0 = row_max(bm0, row_max(x[i][0], x[i][2]));
+        bm1 = row_max(bm1, row_max(x[i][1], x[i][3]));
     }
-    const float f0 = qk_log2 * sK * Q.s0, f1 = qk_log2 * sK * Q.s1;
-    const float eA = bias_log2(eb[rowA]), eB = bias_log2(eb[rowB]);
-    const float x0 = fmaf(sacc[0] + sacc2[0], f0, eA), x1 = fmaf(sacc[1] + sacc2[1], f1, eA);
-    const float x2 = fmaf(sacc[2] + sacc2[2], f0, eB), x3 = fmaf(sacc[3] + sacc2[3], f1, eB);
-    float bm0 = max_nan(x0, x2), bm1 = max_nan(x1, x3);
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) {
-        bm0 = max_nan(bm0, __shfl_xor_sync(0xFFFFFFFFu, bm0, sh));
-        bm1 = max_nan(bm1, __shfl_xor_sync(0xFFFFFFFFu, bm1, sh));
+        bm0 = row_max(bm0, __shfl_xor_sync(0xFFFFFFFFu, bm0, sh));
+        bm1 = row_max(bm1, __shfl_xor_sync(0xFFFFFFFFu, bm1, sh));
     }
-    const float mn0 = max_nan(st.m0, bm0 - kPBias), mn1 = max_nan(st.m1, bm1 - kPBias);
+    const float mn0 = row_max(st.m0, bm0 - bias), mn1 = row_max(st.m1, bm1 - bias);
     const float ms0 = mn0 == kNegInf ? 0.f : mn0, ms1 = mn1 == kNegInf ? 0.f : mn1;  // nothing seen yet: all zeros
-    const float c0 = exp2f(st.m0 - ms0), c1 = exp2f(st.m1 - ms1);
-    const float p0 = exp2f(x0 - ms0), p1 = exp2f(x1 - ms1), p2 = exp2f(x2 - ms0), p3 = exp2f(x3 - ms1);
+    const float c0 = exp2_fast(st.m0 - ms0), c1 = exp2_fast(st.m1 - ms1);
+    float s0 = 0.f, s1 = 0.f;    // of P as it goes into the product: the denominator sums what the numerator sums
+    float w0 = 0.f, w1 = 0.f;    // of P before its rounding
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float p0 = exp2_fast(x[i][0] - ms0), p1 = exp2_fast(x[i][1] - ms1);
+        const float p2 = exp2_fast(x[i][2] - ms0), p3 = exp2_fast(x[i][3] - ms1);
+        const uint32_t lo = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        const uint32_t hi = kF16 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
+        pb[i][0] = movmatrix_trans(lo);
+        pb[i][1] = movmatrix_trans(hi);
+        if constexpr (kWeights) {
+            w0 += p0 + p2;
+            w1 += p1 + p3;
+        } else {
+            const float2 a = kF16 ? unpack_f16x2(lo) : make_float2(bf16_lo(lo), bf16_hi(lo));
+            const float2 b = kF16 ? unpack_f16x2(hi) : make_float2(bf16_lo(hi), bf16_hi(hi));
+            s0 += a.x + b.x;
+            s1 += a.y + b.y;
+        }
+    }
+    // with weights, both sums without P's rounding (which is unbiased: out moves by less than its own last bit)
+    st.l0 = fmaf(st.l0, c0, kWeights ? w0 : s0);
+    st.l1 = fmaf(st.l1, c1, kWeights ? w1 : s1);
     st.m0 = mn0;
     st.m1 = mn1;
-    if constexpr (kWeights) leave_weights(rec, p0 + p2, p1 + p3, ms0, ms1, warp, r, c);
-    // rounded to f16 once; the denominator sums what the numerator sums (kWeights: as attend_block)
-    const uint32_t plo = pack_f16x2(p0, p1), phi = pack_f16x2(p2, p3);
-    const float2 lo = unpack_f16x2(plo), hi = unpack_f16x2(phi);
-    st.l0 = fmaf(st.l0, c0, kWeights ? p0 + p2 : lo.x + hi.x);
-    st.l1 = fmaf(st.l1, c1, kWeights ? p1 + p3 : lo.y + hi.y);
+    if constexpr (kWeights) leave_weights(rec, w0, w1, ms0, ms1, r, c);
     if (__any_sync(0xFFFFFFFFu, c0 != 1.f || c1 != 1.f)) {  // the maximum rises a few times in a long context
 #pragma unroll
         for (int tt = 0; tt < 8; ++tt) {
@@ -141,24 +184,126 @@ __device__ __forceinline__ void attend8(WarpState &st, const Query8 &Q, const ui
             st.o[tt][2] *= c0; st.o[tt][3] *= c1;
         }
     }
-    const uint32_t pb[2] = {movmatrix_trans(plo), movmatrix_trans(phi)};
+}
+
+// One block of codes (t: 64 key rows, then 64 value rows, 128 bytes each, 128-byte swizzle), every
+// token of it before the newest block.  sK, sV: its scales.  kWeights: leave its weights in rec.
+template <int kFmt, bool kWeights>
+__device__ __forceinline__ void attend8(WarpState &st, const Query8 &Q, const uint8_t *t, const float *eb, float sK,
+                                        float sV, float qk_log2, int r, int c, int sig, float *rec) {
+    float x[4][4];
+    // ---- S^T (4 slices of 16 tokens x 8 heads) ----
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint8_t *kp = t + sig * kRow8Bytes + (((c + 4 * j) ^ sig) << 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 ka = lds128(kp + 16 * i * kRow8Bytes), kb = lds128(kp + (16 * i + 8) * kRow8Bytes);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t y = biased<kFmt>(word(ka, w)), z = biased<kFmt>(word(kb, w));
+                const uint32_t a[4] = {codes_lo<kFmt>(y), codes_lo<kFmt>(z), codes_hi<kFmt>(y), codes_hi<kFmt>(z)};
+                mma_16816_f16(x[i], a, Q.f[4 * j + w]);
+            }
+        }
+    }
+    const float f0 = qk_log2 * sK * Q.s0, f1 = qk_log2 * sK * Q.s1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float eA = bias_log2(eb[16 * i + sig]), eB = bias_log2(eb[16 * i + sig + 8]);
+        x[i][0] = fmaf(x[i][0], f0, eA);
+        x[i][1] = fmaf(x[i][1], f1, eA);
+        x[i][2] = fmaf(x[i][2], f0, eB);
+        x[i][3] = fmaf(x[i][3], f1, eB);
+    }
+    uint32_t pb[4][2];
+    softmax_step<true, kWeights, true>(st, x, pb, kPBias, r, c, rec);
     // ---- O^T (128 dims x 8 heads) += s_V C'^T P^T ----
-    const uint8_t *vb = t + kHalfBlock8Bytes + (warp * 16 + c) * kRow8Bytes;
-    const int off0 = ((sig ^ c) << 4), off1 = ((sig ^ (c + 4)) << 4);
-    const uint4 v0 = lds128(vb + off0), v1 = lds128(vb + 4 * kRow8Bytes + off1);
-    const uint4 v2 = lds128(vb + 8 * kRow8Bytes + off0), v3 = lds128(vb + 12 * kRow8Bytes + off1);
+    float d[8][4];
 #pragma unroll
-    for (int wi = 0; wi < 4; ++wi) {
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t *vb = t + kHalfBlock8Bytes + (16 * i + c) * kRow8Bytes;
+        const int off0 = ((sig ^ c) << 4), off1 = ((sig ^ (c + 4)) << 4);
+        const uint4 v0 = lds128(vb + off0), v1 = lds128(vb + 4 * kRow8Bytes + off1);
+        const uint4 v2 = lds128(vb + 8 * kRow8Bytes + off0), v3 = lds128(vb + 12 * kRow8Bytes + off1);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // dims 4 wi + 2 half, + 1 of the chunk: bytes of two tokens side by side
-            const uint32_t z = biased<kFmt>(__byte_perm(word(v0, wi), word(v1, wi), half ? 0x7362 : 0x5140));
-            const uint32_t y = biased<kFmt>(__byte_perm(word(v2, wi), word(v3, wi), half ? 0x7362 : 0x5140));
+        for (int tt = 0; tt < 8; ++tt) {  // dims 2 tt, 2 tt + 1 of the chunk: bytes of two tokens side by side
+            const int sel = (tt & 1) ? 0x7362 : 0x5140;
+            const uint32_t z = biased<kFmt>(__byte_perm(word(v0, tt >> 1), word(v1, tt >> 1), sel));
+            const uint32_t y = biased<kFmt>(__byte_perm(word(v2, tt >> 1), word(v3, tt >> 1), sel));
             const uint32_t a[4] = {codes_lo<kFmt>(z), codes_hi<kFmt>(z), codes_lo<kFmt>(y), codes_hi<kFmt>(y)};
-            float d[4];
-            mma_16816_f16_zero(d, a, pb);
-            float(&o)[4] = st.o[2 * wi + half];
+            if (i == 0) mma_16816_f16_zero(d[tt], a, pb[i]);
+            else mma_16816_f16(d[tt], a, pb[i]);
+        }
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = fmaf(d[i], sV, o[i]);
+    for (int tt = 0; tt < 8; ++tt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.o[tt][j] = fmaf(d[tt][j], sV, st.o[tt][j]);
+}
+
+// One bf16 block by one warp (kt: its key rows, vt: its value rows, two boxes each): the tail of an 8-bit store (Dims8: the value loads then have a two-way
+// bank conflict, on one block of a unit), or a block of the bf16 store whose weights are kept.  Tokens
+// at or beyond L are not seen.
+template <class Dims, bool kWeights>
+__device__ __forceinline__ void attend16(WarpState &st, const uint32_t (&qf)[8][2], const uint8_t *kt, const uint8_t *vt,
+                                         const float *eb, int32_t lb, int32_t L, float qk_log2, int r, int c, int sig, float *rec) {
+    constexpr bool kWide = std::is_same<Dims, Dims8>::value;  // chunks 2 sig, 2 sig + 1 of the row
+    const int32_t n = min(L - lb * kBlock, kBlock);            // tokens seen
+    float x[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint8_t *kp = kt + (j >> 1) * kBoxBytes + sig * 128 + (((((j & 1) << 2) + c) ^ sig) << 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 ka = lds128(kp + 16 * i * 128), kb = lds128(kp + (16 * i + 8) * 128);
+            const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y};
+            const uint32_t a1[4] = {ka.z, kb.z, ka.w, kb.w};
+            mma_16816(x[i], a0, qf[2 * j]);
+            mma_16816(x[i], a1, qf[2 * j + 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int rowA = 16 * i + sig, rowB = rowA + 8;
+        const float eA = bias_log2(eb[rowA]), eB = bias_log2(eb[rowB]);
+        x[i][0] = rowA < n ? fmaf(x[i][0], qk_log2, eA) : kNegInf;
+        x[i][1] = rowA < n ? fmaf(x[i][1], qk_log2, eA) : kNegInf;
+        x[i][2] = rowB < n ? fmaf(x[i][2], qk_log2, eB) : kNegInf;
+        x[i][3] = rowB < n ? fmaf(x[i][3], qk_log2, eB) : kNegInf;
+    }
+    uint32_t pb[4][2];
+    softmax_step<kWide, kWeights, false>(st, x, pb, 0.f, r, c, rec);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (16 * i >= n) break;  // every P left is zero
+        const int vt0 = 16 * i + c;
+#pragma unroll
+        for (int bx = 0; bx < 2; ++bx) {
+            const uint8_t *vb = vt + (kWide ? sig >> 2 : bx) * kBoxBytes;
+            const int ch = kWide ? 2 * (sig & 3) + bx : sig;
+            uint4 v0 = lds128(vb + (vt0 + 0) * 128 + ((ch ^ c) << 4));
+            uint4 v1 = lds128(vb + (vt0 + 4) * 128 + ((ch ^ (c + 4)) << 4));
+            uint4 v2 = lds128(vb + (vt0 + 8) * 128 + ((ch ^ c) << 4));
+            uint4 v3 = lds128(vb + (vt0 + 12) * 128 + ((ch ^ (c + 4)) << 4));
+            if (n < kBlock) {  // rows at or beyond L hold stale bits: keep them out of 0 * x
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                if (vt0 >= n) v0 = z;
+                if (vt0 + 4 >= n) v1 = z;
+                if (vt0 + 8 >= n) v2 = z;
+                if (vt0 + 12 >= n) v3 = z;
+            }
+#pragma unroll
+            for (int wi = 0; wi < 4; ++wi) {
+                const uint32_t y0 = word(v0, wi), y1 = word(v1, wi), y2 = word(v2, wi), y3 = word(v3, wi);
+                const uint32_t a[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632),
+                                       __byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+                mma_16816(st.o[4 * bx + wi], a, pb[i]);
+            }
         }
     }
 }

@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32) cache_plan_kernel(const Cache
     }
 }
 
-// kBytes: a block's (32 KiB of bf16 rows, or 16 KiB of codes).
-template <int kBytes>
+// kBytes: a block's (32 KiB of bf16 rows, or a record of codes), kStride: from one to the next.
+template <int kBytes, int kStride>
 __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const CacheParams p) {
     constexpr int kChunksPerBlock = kBytes / 16;
     // No early trigger: the decode that follows would hold most of each SM's
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
         u = lo_u;
         const uint32_t e = p.miss_list[(int64_t)u * p.max_sel + (m - P[u])];
         const int32_t slot = (int32_t)(e >> 20), blk = (int32_t)(e & 0xFFFFFu);
-        const uint8_t *src = p.store + ((int64_t)u * p.nblk + blk) * kBytes;
-        uint8_t *dst = p.cache + ((int64_t)u * p.nslots + slot) * kBytes;
+        const uint8_t *src = p.store + ((int64_t)u * p.nblk + blk) * kStride;
+        uint8_t *dst = p.cache + ((int64_t)u * p.nslots + slot) * kStride;
         const int64_t bend = min(hi, (int64_t)(m + 1) * kChunksPerBlock);
         const int32_t k0 = (int32_t)(c - (int64_t)m * kChunksPerBlock);
         const int32_t k1 = (int32_t)(bend - (int64_t)m * kChunksPerBlock);
@@ -193,7 +193,8 @@ int launch_cache_sync(const CacheParams &p, cudaStream_t stream) {
                    plan_smem, stream, p) != cudaSuccess)
         return NOSA_ERR_CUDA;
     const size_t gather_smem = ((size_t)p.units + 1) * sizeof(int32_t);
-    const auto gather = p.fmt == kFmtBf16 ? cache_gather_kernel<kBlockBytes> : cache_gather_kernel<kBlock8Bytes>;
+    const auto gather = p.fmt == kFmtBf16 ? cache_gather_kernel<kBlockBytes, kBlockBytes>
+                                            : cache_gather_kernel<kHeld8Bytes, kRec8Bytes>;
     return launch_pdl(gather, dim3(kNumSms * kGatherCtasPerSm), dim3(kGatherThreads), gather_smem,
                       stream, p) == cudaSuccess
                ? NOSA_OK

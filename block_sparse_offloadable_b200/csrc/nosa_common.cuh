@@ -26,6 +26,9 @@ constexpr int kBlockBytes = 2 * kHalfBlockBytes;     // keys + values of a block
 constexpr int kRow8Bytes = kD;                // one 8-bit key or value row: 128 B
 constexpr int kHalfBlock8Bytes = kBlock * kRow8Bytes;  // keys (or values) of an 8-bit block: 8 KiB
 constexpr int kBlock8Bytes = 2 * kHalfBlock8Bytes;     // keys + values of an 8-bit block: 16 KiB
+constexpr int kSide8Bytes = kBlock * 4 + 16;           // its 64 logits, s_K, s_V, 8 bytes unused
+constexpr int kHeld8Bytes = kBlock8Bytes + kSide8Bytes;      // a block's record: what is copied
+constexpr int kRec8Bytes = (kHeld8Bytes + 127) / 128 * 128;  // from one record to the next: whole 128-byte lines
 constexpr int kMaxG = 8;                      // query heads per kv head handled by one tile
 constexpr int kMaxKq = 32;                    // Gamma_q fits one warp-wide sorted list
 constexpr int kMaxKe = 256;
@@ -89,6 +92,16 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+
+// 3-D tiled tensor load into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -189,6 +202,13 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 2^x by the hardware's approximation (2 units in the last place), results below 2^-126 as zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 

@@ -49,7 +49,7 @@
 //    the stream, so all four always meet at the same barriers; a bounded wait
 //    that runs out sets a shared abort flag and the error word, and the rest
 //    of the CTA drains without computing.
-#include "nosa_attend8.cuh"
+#include "nosa_decode_work.cuh"
 
 namespace nosa {
 
@@ -59,145 +59,35 @@ namespace {
 // SM together and the two kernels really run concurrently.
 constexpr int kDecS = 6;
 constexpr int kDecSResident = 4;
-// The same for the 8-bit store (half the bytes a stage), and its buffers for bf16 tails.
-constexpr int kDecS8 = 8, kTails8 = 2;
-constexpr int kDecS8Resident = 4, kTails8Resident = 1;
-static_assert(kDecS % kGroups == 0 && kDecSResident % kGroups == 0 && kDecS8 % kGroups == 0 &&
-                  kDecS8Resident % kGroups == 0,
+static_assert(kDecS % kGroups == 0 && kDecSResident % kGroups == 0,
               "stage s must always be consumed by group s % kGroups");
-__host__ __device__ constexpr int stage_bytes(int fmt) { return fmt == kFmtBf16 ? kBlockBytes : kBlock8Bytes; }
-// Work items of unit u in the kernel's mode.
-__device__ __forceinline__ int32_t unit_work(const DecodeParams &p, int32_t u) {
-    const int32_t L = p.seq_len[u];
-    if (L <= 0) return 0;
-    switch (p.mode) {
-    case kModeSel: return max(0, min(p.nsel[u], p.max_sel));
-    case kModeResident: return min(max(p.gamma_n[u], 0), p.k_e) + 1;
-    case kModeRest: return p.k_q;
-    default: return (L + kBlock - 1) / kBlock;
-    }
-}
-
-// Block id (lb; -1 = nothing to attend) and buffer block index (pb) of item j of unit u.
-__device__ __forceinline__ void item_block(const DecodeParams &p, int32_t u, int32_t j, int32_t &lb, int32_t &pb) {
-    if (p.mode == kModeSel) {
-        lb = p.sel[(int64_t)u * p.max_sel + j];
-        pb = p.block_table ? p.block_table[(int64_t)u * p.max_sel + j] : lb;
-        return;
-    }
-    if (p.mode == kModeDense) {
-        lb = pb = j;
-        return;
-    }
-    if (p.mode == kModeResident) {
-        const int32_t ne = min(max(p.gamma_n[u], 0), p.k_e);
-        lb = (j < ne) ? p.gamma_e[(int64_t)u * p.k_e + j] : (p.seq_len[u] - 1) / kBlock;
-    } else {  // kModeRest: Gamma_q entries not already attended by the resident pass
-        lb = p.gq[(int64_t)u * p.k_q + j];
-        if (lb >= 0 && lb < p.nblk &&
-            ((p.res_bits[(int64_t)u * p.bits_words + (lb >> 5)] >> (lb & 31)) & 1u))
-            lb = -1;
-    }
-    pb = (p.block_slot && lb >= 0 && lb < p.nblk) ? p.block_slot[(int64_t)u * p.nblk + lb] : lb;
-}
-
-// Merge the resident pass's state of unit u (head h, dim d) into (M, acc, lsum) in place.
-__device__ __forceinline__ void merge_resident(const DecodeParams &p, int32_t u, int h, int d, float &M, float &acc,
-                                               float &lsum) {
-    const float *r = p.res_part + (int64_t)u * kPartFloats;
-    const float rm = r[h];
-    const float Mn = fmaxf(M, rm);
-    if (Mn == -__builtin_huge_valf()) return;
-    const float fa = (M == -__builtin_huge_valf()) ? 0.f : exp2f(M - Mn);
-    const float fr = (rm == -__builtin_huge_valf()) ? 0.f : exp2f(rm - Mn);
-    acc = fmaf(fr, r[2 * kMaxG + h * kD + d], fa * acc);
-    lsum = fmaf(fr, r[kMaxG + h], fa * lsum);
-    M = Mn;
-}
-
-// Largest u with P[u] <= x, for 0 <= x < P[U] (skips units without work).
-__device__ __forceinline__ int32_t find_unit(const int32_t *P, int32_t U, int64_t x) {
-    int32_t lo = 0, hi = U;
-    while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (P[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-// CTA whose range [c*W/G, (c+1)*W/G) holds item x (every range non-empty: W >= G).
-__device__ __forceinline__ int32_t cta_of(int64_t x, int64_t W, int32_t G) {
-    return (int32_t)(((x + 1) * G - 1) / W);
-}
-
-// Add each of a unit's blocks' weight: the items' values (rec, left by the warps that attended them)
-// against the whole sums' log2 per head.  By all consumer threads of the unit's last CTA.
-__device__ __forceinline__ void add_weights(const DecodeParams &p, int32_t u, int64_t item0, int32_t n,
-                                            const float *s_lse, int ctid) {
-    for (int32_t j = ctid; j < n; j += kConsThreads) {
-        int32_t lb, pb;
-        item_block(p, u, j, lb, pb);
-        if (lb < 0 || (int64_t)lb * kBlock >= p.seq_len[u]) continue;
-        const float4 *rec = reinterpret_cast<const float4 *>(p.rec + (item0 + j) * kRecFloats);
-        float4 v[kRecFloats / 4];
-#pragma unroll
-        for (int i = 0; i < kRecFloats / 4; ++i) v[i] = __ldcg(rec + i);
-        float w = 0.f;
-#pragma unroll
-        for (int h = 0; h < kMaxG; ++h) {
-            const float lse = h < p.G ? s_lse[h] : kNegInf;
-            if (lse == kNegInf) continue;  // a head that sees nothing gives no weight
-#pragma unroll
-            for (int t = 0; t < kDecW; ++t) {
-                const float4 x = v[2 * t + h / 4];
-                w += exp2f((h % 4 == 0 ? x.x : h % 4 == 1 ? x.y : h % 4 == 2 ? x.z : x.w) - lse);
-            }
-        }
-        atomicAdd(p.weights + (int64_t)u * p.nblk + lb, w);  // a caller's list may name a block twice
-    }
-}
-
 }  // namespace
 
-size_t decode_smem_bytes(int32_t units, int fmt, int stages, int tails) {
-    return 1024 + (size_t)stages * stage_bytes(fmt) + (size_t)tails * kBlockBytes +
-           (size_t)stages * kBlock * sizeof(float) + (fmt == kFmtBf16 ? 0 : (size_t)stages * 16) +
-           (2 * stages + tails) * sizeof(uint64_t) + (tails > 0 ? 2 : 1) * stages * sizeof(int32_t) +
-           (size_t)kDecW * kScr * sizeof(float) + ((size_t)units + 1) * sizeof(int32_t);
+size_t decode_smem_bytes(int32_t units, int stages) {
+    return 1024 + (size_t)stages * kBlockBytes + (size_t)stages * kBlock * sizeof(float) +
+           2 * stages * sizeof(uint64_t) + stages * sizeof(int32_t) + (size_t)kDecW * kScr * sizeof(float) +
+           ((size_t)units + 1) * sizeof(int32_t);
 }
 
 int decode_ctas() { return kNumSms; }
 
-// kFmt: the blocks' format.  The 8-bit store's newest block of a unit is in bf16, in a buffer of its
-// own (kTails of them): its item takes a ring stage too, whose barrier its copies complete on.
-// kWeights: add the blocks' weights to p.weights.
-template <int kFmt, int kStages, int kTails, bool kWeights>
+template <int kStages>
 __global__ void __launch_bounds__(kDecThreads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tail_map,
-                  const DecodeParams p) {
-    constexpr bool k8 = kFmt != kFmtBf16;
-    constexpr int kStageBytes = stage_bytes(kFmt);
-    using Dims = std::conditional_t<k8, Dims8, DimsBf16>;
+    decode_kernel(const __grid_constant__ CUtensorMap tmap, const DecodeParams p) {
     pdl_trigger();  // the next append's CTAs are tiny; they wait for this grid
     pdl_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *tails = tiles + kStages * kStageBytes;
-    float *ebuf = reinterpret_cast<float *>(tails + kTails * kBlockBytes);
-    float2 *sbuf = reinterpret_cast<float2 *>(ebuf + kStages * kBlock);  // [stage][2]: scales of blocks 2i, 2i + 1
-    uint64_t *full = reinterpret_cast<uint64_t *>(sbuf + (k8 ? 2 * kStages : 0));
+    float *ebuf = reinterpret_cast<float *>(tiles + kStages * kBlockBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ebuf + kStages * kBlock);
     uint64_t *empty = full + kStages;
-    uint64_t *tempty = empty + kStages;
-    int32_t *s_blk = reinterpret_cast<int32_t *>(tempty + kTails);
-    int32_t *s_tail = s_blk + kStages;  // the tail buffer of a stage's item, or -1 (8-bit store)
-    float *scratch = reinterpret_cast<float *>(s_tail + (k8 ? kStages : 0));
+    int32_t *s_blk = reinterpret_cast<int32_t *>(empty + kStages);
+    float *scratch = reinterpret_cast<float *>(s_blk + kStages);
     int32_t *P = reinterpret_cast<int32_t *>(scratch + kDecW * kScr);
     __shared__ int32_t s_wsum[kConsWarps + 1];
     __shared__ int s_last;
     __shared__ volatile int s_abort;
-    __shared__ float s_lse[kMaxG];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t U = p.units, G = (int32_t)gridDim.x, cta = (int32_t)blockIdx.x;
@@ -207,10 +97,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kDecW);
         }
-        for (int s = 0; s < kTails; ++s) mbar_init(&tempty[s], kDecW);
         fence_mbar_init();
         prefetch_tmap(&tmap);
-        if constexpr (k8) prefetch_tmap(&tail_map);
         s_abort = 0;
     }
     // ---- P[u] = items of units < u ----
@@ -263,66 +151,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     if (warp == kConsWarps) {
         // ---------------- producer ----------------
-        int it = 0, nt = 0;
+        int it = 0;
         for (int64_t xb = lo; xb < hi && !s_abort; xb += 32) {
             const int nb = (int)((hi - xb) < 32 ? (hi - xb) : 32);
-            int32_t blb = -1, bpb = -1, bu = 0, blocal = -1;
+            int32_t blb = -1, bpb = -1, bu = 0;
             if (lane < nb) {
                 const int64_t x = xb + lane;
                 bu = find_unit(P, U, x);
-                if constexpr (k8) blocal = p.seq_len[bu] > 0 ? (p.seq_len[bu] - 1) / kBlock : -1;
                 item_block(p, bu, (int32_t)(x - P[bu]), blb, bpb);
             }
             for (int k = 0; k < nb; ++k, ++it) {
                 const int32_t u = __shfl_sync(0xFFFFFFFFu, bu, k);
                 const int32_t lb = __shfl_sync(0xFFFFFFFFu, blb, k);
                 const int32_t pb = __shfl_sync(0xFFFFFFFFu, bpb, k);
-                const int32_t local = __shfl_sync(0xFFFFFFFFu, blocal, k);
                 if (lane == 0) {
                     const int s = it % kStages;
                     const bool go =
                         it < kStages || wait_or_abort(&empty[s], ((it / kStages) - 1) & 1, &s_abort, p.err);
-                    if constexpr (k8) {
-                        if (go) {
-                            const bool tail = lb >= 0 && lb == local;
-                            const bool ok = tail || (lb >= 0 && lb < local && pb >= 0 && pb < p.blocks_per_unit);
-                            // a block with no buffer; blocks past the newest hold nothing to attend
-                            if (!ok && lb >= 0 && (lb <= local || (int64_t)lb * kBlock >= p.max_ctx))
-                                set_error(p.err, NOSA_EFLAG_STATE);
-                            bool have = ok;
-                            int tb = -1;
-                            if (tail) {
-                                tb = nt % kTails;
-                                if (nt >= kTails)
-                                    have = wait_or_abort(&tempty[tb], ((nt / kTails) - 1) & 1, &s_abort, p.err);
-                                ++nt;
-                            }
-                            s_blk[s] = have ? lb : -1;
-                            s_tail[s] = tb;
-                            const float *e = p.e + (int64_t)u * p.max_ctx + (int64_t)lb * kBlock;
-                            if (have && tail) {
-                                const int32_t y = u * 2 * kBlock;
-                                uint8_t *t = tails + tb * kBlockBytes;
-                                mbar_arrive_expect_tx(&full[s], kBlockBytes + kBlock * sizeof(float));
-                                tma_load_2d(t, &tail_map, &full[s], 0, y);
-                                tma_load_2d(t + kBoxBytes, &tail_map, &full[s], 64, y);
-                                tma_load_2d(t + 2 * kBoxBytes, &tail_map, &full[s], 0, y + kBlock);
-                                tma_load_2d(t + 3 * kBoxBytes, &tail_map, &full[s], 64, y + kBlock);
-                                bulk_load(ebuf + s * kBlock, e, kBlock * sizeof(float), &full[s]);
-                            } else if (have) {
-                                const int32_t y = (int32_t)(((int64_t)u * p.blocks_per_unit + pb) * 2 * kBlock);
-                                uint8_t *t = tiles + s * kStageBytes;
-                                mbar_arrive_expect_tx(&full[s], kStageBytes + kBlock * sizeof(float) + 16);
-                                tma_load_2d(t, &tmap, &full[s], 0, y);
-                                tma_load_2d(t + kHalfBlock8Bytes, &tmap, &full[s], 0, y + kBlock);
-                                bulk_load(ebuf + s * kBlock, e, kBlock * sizeof(float), &full[s]);
-                                bulk_load(sbuf + 2 * s, p.kv8.scales + (int64_t)u * p.kv8.scale_stride + (lb & ~1), 16,
-                                          &full[s]);
-                            } else {
-                                mbar_arrive(&full[s]);
-                            }
-                        }
-                    } else if (go) {
+                    if (go) {
                         const bool ok = lb >= 0 && (int64_t)lb * kBlock < p.max_ctx && pb >= 0 &&
                                         pb < p.blocks_per_unit;
                         s_blk[s] = ok ? lb : -1;
@@ -360,7 +206,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         WarpState st;
         st.reset();
         uint32_t qf[8][2];
-        [[maybe_unused]] Query8 q8;
         int32_t L = 0;
         // a unit's queries (B fragments, dims permuted as the key loads) and length
         auto load_unit = [&](int32_t uu) {
@@ -372,7 +217,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 qf[2 * jj + 1][0] = x.z; qf[2 * jj + 1][1] = x.w;
             }
             L = p.seq_len[uu];
-            if constexpr (k8) load_query8(q8, p.q + (int64_t)uu * p.G * kD, p.G, r, c);
         };
         const int32_t first_unit = n_items > 0 ? find_unit(P, U, lo) : 0;
         int32_t u = first_unit;
@@ -386,24 +230,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 const int s = it % kStages;
                 if (wait_or_abort(&full[s], (it / kStages) & 1, &s_abort, p.err)) {
                     const int32_t lb = s_blk[s];
-                    float *rec = kWeights ? p.rec + xi * kRecFloats : nullptr;
-                    if constexpr (k8) {
-                        const int32_t tb = s_tail[s];
-                        if (lb >= 0 && tb >= 0) {
-                            attend_block<Dims8, kWeights>(st, qf, tails + tb * kBlockBytes, ebuf + s * kBlock, lb, L,
-                                                          p.qk_log2, wq, c, sig, rec, r);
-                        } else if (lb >= 0) {
-                            const float2 sc = sbuf[2 * s + (lb & 1)];
-                            attend8<kFmt, kWeights>(st, q8, tiles + s * kStageBytes, ebuf + s * kBlock, sc.x, sc.y,
-                                                    p.qk_log2, wq, r, c, sig, rec);
-                        }
-                        __syncwarp();
-                        if (lane == 0 && tb >= 0) mbar_arrive(&tempty[tb]);
-                    } else if (lb >= 0) {
-                        attend_block<Dims, kWeights>(st, qf, tiles + s * kBlockBytes, ebuf + s * kBlock, lb, L,
-                                                     p.qk_log2, wq, c, sig, rec, r);
-                    }
-                    if (kWeights && lb < 0) leave_none(rec, wq, r, c);
+                    if (lb >= 0)
+                        attend_block(st, qf, tiles + s * kBlockBytes, ebuf + s * kBlock, lb, L, p.qk_log2,
+                                     wq, c, sig);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
@@ -411,7 +240,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const int32_t u_next = (seg_end < hi) ? find_unit(P, U, seg_end) : u;
 
             // ---- segment end: fold group 0 into group 1 lane by lane, merge the four warps ----
-            fold_groups<Dims>(st, scratch, grp, wq, r, c, sig);
+            fold_groups(st, scratch, grp, wq, r, c, sig);
             if (seg_end < hi) load_unit(u_next);  // in flight while the merge runs
             const int nout = p.G * kD;
             uint16_t *out = p.out + (int64_t)u * p.G * kD;
@@ -419,18 +248,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int idx = ctid; idx < nout; idx += kConsThreads) {
                 const int h = idx >> 7, d = idx & (kD - 1);
                 float M, acc, lsum;
-                merged_state<Dims>(scratch, h, d, M, acc, lsum);
+                merged_state(scratch, h, d, M, acc, lsum);
                 if (whole && p.mode == kModeResident) {
                     store_partial(p.res_part + (int64_t)u * kPartFloats, h, d, M, acc, lsum);
                 } else if (whole) {
                     if (p.mode == kModeRest) merge_resident(p, u, h, d, M, acc, lsum);
-                    store_bf16(out + idx, has_weight<k8>(lsum) ? acc / lsum : 0.f);
-                    if (kWeights && d == 0) s_lse[h] = M + log2f(lsum);
+                    store_bf16(out + idx, lsum > 0.f ? acc / lsum : 0.f);
                 } else {
                     store_partial(part, h, d, M, acc, lsum);
                 }
             }
-            bool add = whole;  // this CTA ends the unit: it adds the weights
             if (!whole) {
                 // hand-off: the partial is written (barrier), one thread counts it with release
                 // semantics; the unit's last contributor acquired the others' partials with the same
@@ -444,8 +271,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     // last piece of the unit: merge the C pieces' partials (piece t: slot 0 of CTA
                     // cf + t) in one pass, every thread loading what its 4 dims need at once
                     if (ctid == 0) p.counter[u] = 0;
-                    merge_pieces_onepass<kFewPieces, k8>(p.part + (int64_t)cf * 2 * kPartFloats, 2 * kPartFloats, C,
-                                                         p.G, out, ctid, kWeights ? s_lse : nullptr);
+                    merge_pieces_onepass(p.part + (int64_t)cf * 2 * kPartFloats, 2 * kPartFloats, C, p.G, out, ctid);
                 } else if (s_last) {
                     // last contributor: merge the unit's partials in CTA order
                     if (ctid == 0) p.counter[u] = 0;
@@ -462,16 +288,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         }
                     }
                     consumer_sync();
-                    merge_general<k8>(ms, nc, p.G, out,
+                    merge_general(ms, nc, p.G, out,
                                   p.mode == kModeResident ? p.res_part + (int64_t)u * kPartFloats : nullptr, warp,
                                   lane, ctid);
-                    if (kWeights && ctid < p.G) s_lse[ctid] = ms.Ms[ctid] + log2f(ms.lsum[ctid]);
                 }
-                add = s_last;
-            }
-            if constexpr (kWeights) {
-                consumer_sync();
-                if (add) add_weights(p, u, P[u], P[u + 1] - P[u], s_lse, ctid);
             }
             consumer_sync();  // scratch and s_last are reused by the next segment
             st.reset();
@@ -491,7 +311,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int idx = ctid; idx < p.G * kD; idx += kConsThreads) {
                 float M = kNegInf, acc = 0.f, lsum = 0.f;
                 if (p.mode == kModeRest) merge_resident(p, uz, idx >> 7, idx & (kD - 1), M, acc, lsum);
-                store_bf16(out + idx, has_weight<k8>(lsum) ? acc / lsum : 0.f);
+                store_bf16(out + idx, lsum > 0.f ? acc / lsum : 0.f);
             }
         }
         // the resident pass also leaves, per unit, the set it covered (for the rest pass)
@@ -511,32 +331,22 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
 }
 
-template <int kFmt, int kStages, int kTails, bool kWeights>
-int launch_decode_t(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream) {
-    const auto kernel = decode_kernel<kFmt, kStages, kTails, kWeights>;
-    const size_t smem = decode_smem_bytes(p.units, kFmt, kStages, kTails);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+template <int kStages>
+int launch_decode_t(const DecodeParams &p, const CUtensorMap &tmap, cudaStream_t stream) {
+    const size_t smem = decode_smem_bytes(p.units, kStages);
+    if (cudaFuncSetAttribute(decode_kernel<kStages>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
         return NOSA_ERR_CUDA;
     const int grid = p.pieces > 0 ? p.units * p.pieces : decode_ctas();
-    return launch_pdl(kernel, dim3(grid), dim3(kDecThreads), smem, stream, tmap, tail_map, p) == cudaSuccess
+    return launch_pdl(decode_kernel<kStages>, dim3(grid), dim3(kDecThreads), smem, stream, tmap, p) ==
+                   cudaSuccess
                ? NOSA_OK
                : NOSA_ERR_CUDA;
 }
 
-template <int kFmt>
-int launch_decode8(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream) {
-    if (p.mode == kModeResident)
-        return launch_decode_t<kFmt, kDecS8Resident, kTails8Resident, false>(p, tmap, tail_map, stream);
-    return p.weights ? launch_decode_t<kFmt, kDecS8, kTails8, true>(p, tmap, tail_map, stream)
-                     : launch_decode_t<kFmt, kDecS8, kTails8, false>(p, tmap, tail_map, stream);
-}
-
-int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream) {
-    if (p.fmt == kFmtInt8) return launch_decode8<kFmtInt8>(p, tmap, tail_map, stream);
-    if (p.fmt == kFmtE4m3) return launch_decode8<kFmtE4m3>(p, tmap, tail_map, stream);
-    if (p.weights) return launch_decode_t<kFmtBf16, kDecS, 0, true>(p, tmap, tail_map, stream);
-    return p.mode == kModeResident ? launch_decode_t<kFmtBf16, kDecSResident, 0, false>(p, tmap, tail_map, stream)
-                                   : launch_decode_t<kFmtBf16, kDecS, 0, false>(p, tmap, tail_map, stream);
+int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, cudaStream_t stream) {
+    return p.mode == kModeResident ? launch_decode_t<kDecSResident>(p, tmap, stream)
+                                   : launch_decode_t<kDecS>(p, tmap, stream);
 }
 
 }  // namespace nosa

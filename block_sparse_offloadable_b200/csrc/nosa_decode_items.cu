@@ -1,0 +1,556 @@
+// nosa_decode_items.cu -- steps a5 and a6 over the 8-bit KV store, and over any store when the blocks'
+// attention weights are kept.
+//
+// NOSA pages: gist.science summary of arXiv:2510.13602, "ED-DMA" (the eviction score enters the
+// softmax as the additive logit e_j); montaan.com "Empirical Results and Analysis" item 4 (decoding
+// is bound by KV loading).  Neither the 8-bit store nor eviction by attention weight is on the pages.
+//
+// The split of nosa_decode.cu's kernel (work items are (unit, block) pairs; equal pieces of a unit
+// per CTA where the units are fewer than the SMs, else balanced ranges; partial states merged by a
+// unit's last CTA), with a different inside, since an 8-bit block is half the bytes and more
+// instructions than a bf16 one:
+//  * One consumer warp attends a whole block (nosa_attend8.cuh).  Five of them (three over the bf16
+//    store) with two stages each: a stage's next block is in flight while its other one is
+//    attended.  Eight warps with ten stages leave two blocks in flight while all attend: 93 us
+//    where this takes 75 at 32 ragged sequences of up to 32K (e4m3, 16 q / 2 kv heads).
+//  * Two producer warps, for the even and the odd items: one issue (expected bytes, a tensor copy of
+//    the codes, a bulk copy of the logits and scales) takes 0.27 us of one thread's time, and a
+//    block must come every 0.38 us to keep the memory busy; the first items are issued by the
+//    consumer warps and the producers at once.
+//  * The newest block of a unit (bf16 tail of the 8-bit store) takes longest and comes first.
+//  * Seven warps leave 255 registers a thread: attend8 wants about 200.
+#include "nosa_attend8.cuh"
+#include "nosa_decode_work.cuh"
+
+namespace nosa {
+
+namespace {
+
+constexpr int kItemCons = 5;                       // consumer warps
+constexpr int kItemProd = 2;                       // producer warps
+constexpr int kItemConsThreads = kItemCons * 32;
+constexpr int kItemThreads = (kItemCons + kItemProd) * 32;
+
+// Stages, and consumer warps that take items (two stages each; stage s always belongs to consumer
+// s % kTakers and producer s % 2, so that every barrier has one waiter, which meets its phases in
+// order: a parity cannot tell phase n from n - 2).  The resident pass of the split decode leaves
+// room for a select CTA on the SM.
+template <int kFmt, bool kResident>
+struct ItemGeo {
+    static constexpr bool k8 = kFmt != kFmtBf16;
+    static constexpr int kStages = (k8 && !kResident) ? 10 : 6;
+    static constexpr int kTakers = kStages / 2;
+    static constexpr int kStageBytes = k8 ? kBlock8Bytes : kBlockBytes;
+    static constexpr int kTails = !k8 ? 0 : (kResident ? 1 : 2);  // buffers for a tail's values (its keys take a stage)
+    static constexpr int kSide = k8 ? kSide8Bytes / 4 : kBlock;   // floats a stage: logits (8-bit store: and scales)
+    static_assert(kTakers <= kItemCons && kStages % kItemProd == 0, "one waiter per barrier");
+
+    static size_t smem_bytes(int32_t prefix) {
+        return 1024 + (size_t)kStages * kStageBytes + (size_t)kTails * kHalfBlockBytes +
+               (size_t)kStages * kSide * sizeof(float) + (2 * kStages + 2) * sizeof(uint64_t) +
+               (size_t)kStages * sizeof(int4) + (size_t)kTakers * kScr * sizeof(float) +
+               (size_t)prefix * sizeof(int32_t);
+    }
+};
+
+// Wait until *at == n (shared memory, written by another warp); false if the bound ran out.
+__device__ __forceinline__ bool reached_or_abort(const volatile int32_t *at, int32_t n, volatile int *abort_flag,
+                                                 uint32_t *err) {
+    const long long t0 = clock64();
+    while (*at != n) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *abort_flag = 1;
+            set_error(err, NOSA_EFLAG_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Segment end, first half: this warp's (m, l, o) to its slot of the scratch.
+template <class Dims>
+__device__ __forceinline__ void leave_state(const WarpState &st, float *mine, int r, int c, int sig) {
+    float l0 = st.l0, l1 = st.l1;
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1) {
+        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, sh);
+        l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, sh);
+    }
+    if (r == 0) {
+        mine[2 * c] = st.m0; mine[2 * c + 1] = st.m1;
+        mine[kMaxG + 2 * c] = l0; mine[kMaxG + 2 * c + 1] = l1;
+    }
+    float *oo = mine + 2 * kMaxG;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const int psi = Dims::psi(t, sig);
+        oo[(2 * c) * kHS + Dims::at(psi)] = st.o[t][0];
+        oo[(2 * c + 1) * kHS + Dims::at(psi)] = st.o[t][1];
+        oo[(2 * c) * kHS + Dims::at(psi + 1)] = st.o[t][2];
+        oo[(2 * c + 1) * kHS + Dims::at(psi + 1)] = st.o[t][3];
+    }
+}
+
+// Second half, for head h and dims d .. d + 3: the warps' states merged into (M, acc, lsum).
+template <class Dims, int kTakers>
+__device__ __forceinline__ void join_states(const float *scratch, int h, int d, float &M, float4 &acc, float &lsum) {
+    M = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kTakers; ++w) M = fmaxf(M, scratch[w * kScr + h]);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTakers; ++w) {
+        const float mw = scratch[w * kScr + h];
+        const float f = (mw == kNegInf) ? 0.f : exp2f(mw - M);
+        const float *o = scratch + w * kScr + 2 * kMaxG + h * kHS;
+        acc.x = fmaf(f, o[Dims::at(d)], acc.x);
+        acc.y = fmaf(f, o[Dims::at(d + 1)], acc.y);
+        acc.z = fmaf(f, o[Dims::at(d + 2)], acc.z);
+        acc.w = fmaf(f, o[Dims::at(d + 3)], acc.w);
+        lsum = fmaf(f, scratch[w * kScr + kMaxG + h], lsum);
+    }
+}
+
+// merge_resident for dims d4 .. d4 + 3.
+__device__ __forceinline__ void merge_resident4(const DecodeParams &p, int32_t u, int h, int d4, float &M, float4 &acc,
+                                                float &lsum) {
+    float m = M, l = lsum;
+    merge_resident(p, u, h, d4, m, acc.x, l);
+    m = M, l = lsum;
+    merge_resident(p, u, h, d4 + 1, m, acc.y, l);
+    m = M, l = lsum;
+    merge_resident(p, u, h, d4 + 2, m, acc.z, l);
+    merge_resident(p, u, h, d4 + 3, M, acc.w, lsum);
+}
+
+// Add each of a unit's blocks' weight: the items' values (rec, left by the warps that attended them)
+// against the whole sums' log2 per head.  By all consumer threads of the unit's last CTA.
+__device__ __forceinline__ void add_weights(const DecodeParams &p, int32_t u, int32_t item0, int32_t n,
+                                            const float *s_lse, int ctid) {
+    for (int32_t j = ctid; j < n; j += kItemConsThreads) {
+        int32_t lb, pb;
+        item_block(p, u, n - 1 - j, lb, pb);  // the items' order, see below
+        if (lb < 0 || (int64_t)lb * kBlock >= p.seq_len[u]) continue;
+        const float4 *rec = reinterpret_cast<const float4 *>(p.rec + (int64_t)(item0 + j) * kRecFloats);
+        const float4 a = __ldcg(rec), b = __ldcg(rec + 1);
+        const float v[kMaxG] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        float w = 0.f;
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h)  // a head that sees nothing gives no weight
+            if (h < p.G && s_lse[h] != kNegInf) w += exp2f(v[h] - s_lse[h]);
+        atomicAdd(p.weights + (int64_t)u * p.nblk + lb, w);  // a caller's list may name a block twice
+    }
+}
+
+// An item: its unit, the unit's length, the block's number (-1: nothing) and its place in the buffer.
+struct Item {
+    int32_t u, L, lb, pb;
+    __device__ __forceinline__ int32_t local() const { return L > 0 ? (L - 1) / kBlock : -1; }
+    __device__ __forceinline__ bool tail() const { return lb >= 0 && lb == local(); }
+};
+
+}  // namespace
+
+// Pieces (p.pieces > 0) only with kModeSel.
+template <int kFmt, bool kWeights, bool kResident>
+__global__ void __launch_bounds__(kItemThreads, 1)
+    decode_items_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap tail_map,
+                        const DecodeParams p) {
+    using Geo = ItemGeo<kFmt, kResident>;
+    constexpr bool k8 = Geo::k8;
+    constexpr int kStages = Geo::kStages, kTakers = Geo::kTakers, kStageBytes = Geo::kStageBytes, kTails = Geo::kTails,
+                  kSide = Geo::kSide;
+    using Dims = std::conditional_t<k8, Dims8, DimsBf16>;
+    pdl_trigger();  // the next append's CTAs are tiny; they wait for this grid
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *tails = tiles + kStages * kStageBytes;
+    float *ebuf = reinterpret_cast<float *>(tails + kTails * kHalfBlockBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ebuf + kStages * kSide);
+    uint64_t *empty = full + kStages;
+    uint64_t *tempty = empty + kStages;
+    int4 *s_item = reinterpret_cast<int4 *>(tempty + 2);  // what a stage holds: (block number, tail buffer or -1, -, -)
+    float *scratch = reinterpret_cast<float *>(s_item + kStages);
+    int32_t *P = reinterpret_cast<int32_t *>(scratch + kTakers * kScr);
+    __shared__ int32_t s_wsum[kItemThreads / 32];
+    __shared__ volatile int32_t s_tail_no[2];  // the tail last issued into each buffer
+    __shared__ int s_last;
+    __shared__ volatile int s_abort;
+    __shared__ float s_lse[kMaxG];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t U = p.units, grid = (int32_t)gridDim.x, cta = (int32_t)blockIdx.x;
+    const bool nominal = p.mode == kModeSel;  // max_sel items per unit, whatever nsel (-1 padded past it)
+
+    if (warp == kItemCons) {
+        if (lane < kStages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
+        }
+        if (lane < kTails) {
+            mbar_init(&tempty[lane], 1);
+            s_tail_no[lane] = lane - kTails;
+        }
+        fence_mbar_init();
+        if (lane == 0) {
+            prefetch_tmap(&tmap);
+            if (k8) prefetch_tmap(&tail_map);
+            s_abort = 0;
+        }
+    }
+    // ---- items of units < u ----
+    if (nominal) {
+        __syncthreads();
+        pdl_wait();  // nothing before it reads global memory
+    } else {
+        pdl_wait();
+        const int per = (U + kItemThreads - 1) / kItemThreads;
+        const int u0 = min((int)threadIdx.x * per, U), u1 = min(u0 + per, U);
+        int32_t sum = 0;
+        for (int u = u0; u < u1; ++u) {
+            const int32_t w = unit_work(p, u);
+            P[u + 1] = w;
+            sum += w;
+        }
+        int32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) s_wsum[warp] = incl;
+        __syncthreads();
+        int32_t run = incl - sum;
+        for (int w = 0; w < warp; ++w) run += s_wsum[w];
+        for (int u = u0; u < u1; ++u) {
+            run += P[u + 1];
+            P[u + 1] = run;
+        }
+        if (threadIdx.x == 0) P[0] = 0;
+        __syncthreads();
+    }
+    const auto first_item = [&](int32_t u) { return nominal ? u * p.max_sel : P[u]; };
+    const auto unit_of = [&](int32_t x) { return nominal ? x / p.max_sel : find_unit(P, U, x); };
+    const int32_t W = first_item(U);  // < 2^25
+    // Balanced: ranges over Ge CTAs, none with fewer items than consumer warps (but for the rest of
+    // the division) -- a CTA with one item costs a merge of its state and saves nothing.
+    const int32_t C = p.pieces;
+    const int32_t We = (W + kTakers - 1) / kTakers;
+    const int32_t Ge = min(max(We, 1), grid);
+    int32_t lo, hi;
+    if (C > 0) {
+        const int32_t rc = cta % C;
+        lo = cta / C * p.max_sel + rc * p.max_sel / C;
+        hi = cta / C * p.max_sel + (rc + 1) * p.max_sel / C;
+    } else {
+        lo = (int32_t)((cta < Ge) ? (int64_t)cta * W / Ge : W);
+        hi = (int32_t)((cta < Ge) ? (int64_t)(cta + 1) * W / Ge : W);
+    }
+    const int32_t n_items = hi - lo;
+
+    // The lanes of a warp look up 32 items at a time.  A unit's items run from its last block to its first.
+    const auto look_up = [&](int32_t x) {
+        Item i = {0, 0, -1, -1};
+        if (x < hi) {
+            i.u = unit_of(x);
+            i.L = p.seq_len[i.u];  // in flight with the block number
+            item_block(p, i.u, first_item(i.u + 1) - 1 - x, i.lb, i.pb);
+        }
+        return i;
+    };
+    // Item number `it` of the CTA, by one thread; nt: the tails before it.
+    const auto issue = [&](const Item &i, int it, int nt) {
+        const int s = it % kStages;
+        uint8_t *t = tiles + s * kStageBytes;
+        float *es = ebuf + s * kSide;
+        if (it >= kStages && !wait_or_abort(&empty[s], ((it / kStages) - 1) & 1, &s_abort, p.err)) return;
+        const bool held = i.pb >= 0 && i.pb < p.blocks_per_unit;
+        if constexpr (!k8) {
+            const bool ok = i.lb >= 0 && (int64_t)i.lb * kBlock < p.max_ctx && held;
+            if (!ok && i.lb >= 0) set_error(p.err, NOSA_EFLAG_STATE);  // a block with no buffer
+            s_item[s].x = ok ? i.lb : -1;
+            if (ok) {
+                const int32_t y = (int32_t)(((int64_t)i.u * p.blocks_per_unit + i.pb) * 2 * kBlock);
+                mbar_arrive_expect_tx(&full[s], kBlockBytes + kBlock * sizeof(float));
+                tma_load_2d(t, &tmap, &full[s], 0, y);
+                tma_load_2d(t + kBoxBytes, &tmap, &full[s], 64, y);
+                tma_load_2d(t + 2 * kBoxBytes, &tmap, &full[s], 0, y + kBlock);
+                tma_load_2d(t + 3 * kBoxBytes, &tmap, &full[s], 64, y + kBlock);
+                bulk_load(es, p.e + (int64_t)i.u * p.max_ctx + (int64_t)i.lb * kBlock, kBlock * sizeof(float), &full[s]);
+            } else {
+                mbar_arrive(&full[s]);
+            }
+        } else if (i.tail()) {
+            constexpr int kT = kTails ? kTails : 1;
+            const int tb = nt % kT;
+            // The buffer's phases in order, whichever producer has the tail: the tail before it in
+            // this buffer has been issued, then consumed.
+            bool have = true;
+            if (nt >= kTails)
+                have = reached_or_abort(&s_tail_no[tb], nt - kT, &s_abort, p.err) &&
+                       wait_or_abort(&tempty[tb], ((nt / kT) - 1) & 1, &s_abort, p.err);
+            s_item[s] = make_int4(have ? i.lb : -1, tb, 0, 0);
+            if (have) {
+                s_tail_no[tb] = nt;
+                const int32_t y = i.u * 2 * kBlock;
+                uint8_t *tv = tails + tb * kHalfBlockBytes;
+                mbar_arrive_expect_tx(&full[s], kBlockBytes + kBlock * sizeof(float));
+                tma_load_2d(t, &tail_map, &full[s], 0, y);
+                tma_load_2d(t + kBoxBytes, &tail_map, &full[s], 64, y);
+                tma_load_2d(tv, &tail_map, &full[s], 0, y + kBlock);
+                tma_load_2d(tv + kBoxBytes, &tail_map, &full[s], 64, y + kBlock);
+                bulk_load(es, p.e + (int64_t)i.u * p.max_ctx + (int64_t)i.lb * kBlock, kBlock * sizeof(float), &full[s]);
+            } else {
+                mbar_arrive(&full[s]);
+            }
+        } else {
+            const bool ok = i.lb >= 0 && i.lb < i.local() && held;
+            // a block with no buffer; blocks past the newest hold nothing to attend
+            if (!ok && i.lb >= 0 && (i.lb < i.local() || (int64_t)i.lb * kBlock >= p.max_ctx))
+                set_error(p.err, NOSA_EFLAG_STATE);
+            s_item[s] = make_int4(ok ? i.lb : -1, -1, 0, 0);
+            if (ok) {
+                const int64_t rb = (int64_t)i.u * p.blocks_per_unit + i.pb;
+                mbar_arrive_expect_tx(&full[s], kHeld8Bytes);
+                tma_load_3d(t, &tmap, &full[s], 0, 0, (int32_t)rb);
+                bulk_load(es, p.records + rb * kRec8Bytes + kBlock8Bytes, kSide8Bytes, &full[s]);
+            } else {
+                mbar_arrive(&full[s]);
+            }
+        }
+    };
+    // Each consumer warp issues its own first item where that waits for nothing (a consumer that waited
+    // for a tail's buffer could hold up the one that frees it).
+    const auto by_consumer = [&](const Item &i, int it, int nt) {
+        return it < kTakers && !(k8 && i.tail() && nt >= kTails);
+    };
+
+    if (warp >= kItemCons) {
+        // ---------------- producers ----------------
+        const int odd = warp - kItemCons;
+        int it = 0, nt = 0;
+        Item next = look_up(lo + lane);  // the next batch, looked up while one is issued
+        for (int32_t xb = lo; xb < hi && !s_abort; xb += 32) {
+            const int nb = min(hi - xb, 32);
+            const Item mine = next;
+            next = look_up(xb + 32 + lane);
+            const unsigned tail_lanes = __ballot_sync(0xFFFFFFFFu, mine.tail());
+            const int my_nt = nt + __popc(tail_lanes & ((1u << lane) - 1u));
+            nt += __popc(tail_lanes);
+            for (int k = 0; k < nb; ++k, ++it) {
+                if (lane == k && it % kItemProd == odd && !by_consumer(mine, it, my_nt)) issue(mine, it, my_nt);
+                __syncwarp();
+            }
+        }
+        // never leave with copies in flight
+        if (lane == 0)
+            for (int i = max(0, it - kStages); i < it; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
+    } else {
+        // ---------------- consumers ----------------
+        const int r = lane >> 2, c = lane & 3;
+        const int sig = (r >> 1) + ((r & 1) << 2);  // row permutation 0,4,1,5,2,6,3,7
+        const int ctid = threadIdx.x;                // 0..kItemConsThreads-1
+        {
+            const Item mine = look_up(lane < kTakers ? lo + lane : hi);
+            const unsigned tail_lanes = __ballot_sync(0xFFFFFFFFu, mine.tail());
+            const int nt = __popc(tail_lanes & ((1u << lane) - 1u));
+            if (lane == warp && warp < n_items && by_consumer(mine, warp, nt)) issue(mine, warp, nt);
+            __syncwarp();
+        }
+        WarpState st;
+        st.reset();
+        uint32_t qf[8][2];
+        [[maybe_unused]] Query8 q8;
+        int32_t L = 0;
+        // a unit's queries (B fragments, dims permuted as the key loads) and length
+        auto load_q = [&](int32_t uu) {
+            const uint4 *qrow = reinterpret_cast<const uint4 *>(p.q + ((int64_t)uu * p.G + r) * kD);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const uint4 x = (r < p.G) ? qrow[4 * jj + c] : make_uint4(0, 0, 0, 0);
+                qf[2 * jj][0] = x.x; qf[2 * jj][1] = x.y;
+                qf[2 * jj + 1][0] = x.z; qf[2 * jj + 1][1] = x.w;
+            }
+        };
+        auto load_unit = [&](int32_t uu) {
+            if constexpr (k8) load_query8(q8, p.q + (int64_t)uu * p.G * kD, p.G, r, c);
+            else load_q(uu);
+            L = p.seq_len[uu];
+        };
+        const int32_t first_unit = n_items > 0 ? unit_of(lo) : 0;
+        int32_t u = first_unit;
+        if (n_items > 0) load_unit(u);
+        for (int32_t x = lo; x < hi;) {
+            const int32_t u_begin = first_item(u), u_end = first_item(u + 1);
+            const int32_t seg_end = min(hi, u_end);
+            const bool whole = x == u_begin && seg_end == u_end;
+            const int slot = (u == first_unit) ? 0 : 1;
+            if (warp < kTakers) {
+                for (int32_t xi = x + ((warp - (x - lo)) % kTakers + kTakers) % kTakers; xi < seg_end; xi += kTakers) {
+                    const int it = xi - lo;
+                    const int s = it % kStages;
+                    if (wait_or_abort(&full[s], (it / kStages) & 1, &s_abort, p.err)) {
+                        const int32_t lb = s_item[s].x, tb = k8 ? s_item[s].y : -1;
+                        float *rec = kWeights ? p.rec + (int64_t)xi * kRecFloats : nullptr;
+                        const uint8_t *t = tiles + s * kStageBytes;
+                        const float *e = ebuf + s * kSide;
+                        if (lb < 0) {
+                            if (kWeights) leave_none(rec, r, c);
+                        } else if constexpr (k8) {
+                            if (tb >= 0) {
+                                load_q(u);  // once a unit
+                                attend16<Dims, kWeights>(st, qf, t, tails + tb * kHalfBlockBytes, e, lb, L, p.qk_log2,
+                                                         r, c, sig, rec);
+                            } else {
+                                attend8<kFmt, kWeights>(st, q8, t, e, e[kBlock], e[kBlock + 1], p.qk_log2, r, c, sig,
+                                                        rec);
+                            }
+                        } else {
+                            attend16<Dims, kWeights>(st, qf, t, t + kHalfBlockBytes, e, lb, L, p.qk_log2, r, c, sig,
+                                                     rec);
+                        }
+                        __syncwarp();
+                        if (lane == 0 && tb >= 0) mbar_arrive(&tempty[tb]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[s]);
+                }
+                leave_state<Dims>(st, scratch + warp * kScr, r, c, sig);
+            }
+            const int32_t u_next = (seg_end < hi) ? unit_of(seg_end) : u;
+            consumer_sync<kItemConsThreads>();
+            if (seg_end < hi) load_unit(u_next);  // in flight while the states are joined
+            uint16_t *out = p.out + (int64_t)u * p.G * kD;
+            float *part = p.part + ((int64_t)cta * 2 + slot) * kPartFloats;
+            for (int v = ctid; v < p.G * (kD / 4); v += kItemConsThreads) {
+                const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
+                float M, lsum;
+                float4 acc;
+                join_states<Dims, kTakers>(scratch, h, d4, M, acc, lsum);
+                if (whole && !kResident) {
+                    if (p.mode == kModeRest) merge_resident4(p, u, h, d4, M, acc, lsum);
+                    *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<k8>(acc, lsum);
+                    if (kWeights && d4 == 0) s_lse[h] = M + log2f(lsum);
+                } else {
+                    float *rec = whole ? p.res_part + (int64_t)u * kPartFloats : part;
+                    *reinterpret_cast<float4 *>(rec + 2 * kMaxG + h * kD + d4) = acc;
+                    if (d4 == 0) {
+                        rec[h] = M;
+                        rec[kMaxG + h] = lsum;
+                    }
+                }
+            }
+            bool add = whole;  // this CTA ends the unit: it adds the weights
+            consumer_sync<kItemConsThreads>();
+            if (!whole) {
+                // hand-off: the partial is written (barrier), one thread counts it with release
+                // semantics; the unit's last contributor acquired the others' partials with the same
+                // atomic, and the barrier after it orders every thread's loads below after them
+                const int32_t cf = C > 0 ? u * C : cta_of(u_begin, W, Ge);
+                const int32_t cl = C > 0 ? u * C + C - 1 : cta_of((int64_t)u_end - 1, W, Ge);
+                if (ctid == 0) s_last = ((int32_t)atom_add_acq_rel_gpu(p.counter + u, 1u) == cl - cf);
+                consumer_sync<kItemConsThreads>();
+                add = s_last;
+                if (s_last && C > 0 && C <= kOnePassPieces) {
+                    // the C pieces' partials (piece t: slot 0 of CTA cf + t) in one pass
+                    if (ctid == 0) p.counter[u] = 0;
+                    merge_pieces_onepass<kFewPieces, k8, kItemConsThreads>(
+                        p.part + (int64_t)cf * 2 * kPartFloats, 2 * kPartFloats, C, p.G, out, ctid,
+                        kWeights ? s_lse : nullptr);
+                } else if (s_last) {
+                    if (ctid == 0) p.counter[u] = 0;
+                    // the CTA partials in CTA order (and, merging the rest pass, the resident state)
+                    const int nc = cl - cf + 1 + (p.mode == kModeRest ? 1 : 0);  // <= Ge + 1
+                    const MergeScratch ms = merge_scratch(scratch, nc);
+                    for (int t = ctid; t < nc; t += kItemConsThreads) {
+                        const int32_t cc = cf + t;
+                        if (cc > cl) {
+                            ms.src[t] = p.res_part + (int64_t)u * kPartFloats;
+                        } else {
+                            const int sl = (C > 0 || unit_of((int32_t)((int64_t)cc * W / Ge)) == u) ? 0 : 1;
+                            ms.src[t] = p.part + (int64_t)(cc * 2 + sl) * kPartFloats;
+                        }
+                    }
+                    consumer_sync<kItemConsThreads>();
+                    merge_general<k8, kItemConsThreads>(
+                        ms, nc, p.G, out, kResident ? p.res_part + (int64_t)u * kPartFloats : nullptr, warp, lane, ctid);
+                    if (kWeights && ctid < p.G) s_lse[ctid] = ms.Ms[ctid] + log2f(ms.lsum[ctid]);
+                }
+                consumer_sync<kItemConsThreads>();  // scratch and s_last are reused by the next segment
+            }
+            if (kWeights && add) {
+                add_weights(p, u, u_begin, u_end - u_begin, s_lse, ctid);
+                consumer_sync<kItemConsThreads>();
+            }
+            st.reset();
+            x = seg_end;
+            u = u_next;
+        }
+        // units without work, one CTA each: zero output (an empty state in the
+        // resident pass; the resident state alone in the rest pass)
+        for (int32_t uz = cta; uz < U; uz += grid) {
+            if (first_item(uz + 1) != first_item(uz)) continue;
+            if (kResident) {
+                float *rp = p.res_part + (int64_t)uz * kPartFloats;
+                for (int i = ctid; i < kPartFloats; i += kItemConsThreads) rp[i] = (i < kMaxG) ? kNegInf : 0.f;
+                continue;
+            }
+            uint16_t *out = p.out + (int64_t)uz * p.G * kD;
+            for (int v = ctid; v < p.G * (kD / 4); v += kItemConsThreads) {
+                float M = kNegInf, lsum = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
+                if (p.mode == kModeRest) merge_resident4(p, uz, h, d4, M, acc, lsum);
+                *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<k8>(acc, lsum);
+            }
+        }
+        // the resident pass also leaves, per unit, the set it covered (for the rest pass)
+        if (kResident) {
+            for (int32_t uz = cta; uz < U; uz += grid) {
+                uint32_t *bits = p.res_bits + (int64_t)uz * p.bits_words;
+                for (int i = ctid; i < p.bits_words; i += kItemConsThreads) bits[i] = 0u;
+                consumer_sync<kItemConsThreads>();
+                const int32_t Lz = p.seq_len[uz];
+                const int32_t ne = Lz > 0 ? min(max(p.gamma_n[uz], 0), p.k_e) : -1;
+                for (int j = ctid; j <= ne; j += kItemConsThreads) {
+                    const int32_t b = (j < ne) ? p.gamma_e[(int64_t)uz * p.k_e + j] : (Lz - 1) / kBlock;
+                    if (b >= 0 && b < p.nblk) atomicOr(&bits[b >> 5], 1u << (b & 31));
+                }
+            }
+        }
+    }
+}
+
+namespace {
+
+template <int kFmt, bool kWeights, bool kResident>
+int launch_items(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream) {
+    const auto kernel = decode_items_kernel<kFmt, kWeights, kResident>;
+    const size_t smem = ItemGeo<kFmt, kResident>::smem_bytes(p.mode == kModeSel ? 0 : p.units + 1);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return NOSA_ERR_CUDA;
+    const int grid = p.pieces > 0 ? p.units * p.pieces : decode_ctas();
+    return launch_pdl(kernel, dim3(grid), dim3(kItemThreads), smem, stream, tmap, tail_map, p) == cudaSuccess
+               ? NOSA_OK
+               : NOSA_ERR_CUDA;
+}
+
+template <int kFmt>
+int launch_items8(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream) {
+    if (p.mode == kModeResident) return launch_items<kFmt, false, true>(p, tmap, tail_map, stream);
+    return p.weights ? launch_items<kFmt, true, false>(p, tmap, tail_map, stream)
+                     : launch_items<kFmt, false, false>(p, tmap, tail_map, stream);
+}
+
+}  // namespace
+
+int launch_decode_items(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream) {
+    if (p.fmt == kFmtInt8) return launch_items8<kFmtInt8>(p, tmap, tail_map, stream);
+    if (p.fmt == kFmtE4m3) return launch_items8<kFmtE4m3>(p, tmap, tail_map, stream);
+    return launch_items<kFmtBf16, true, false>(p, tmap, tail_map, stream);
+}
+
+}  // namespace nosa

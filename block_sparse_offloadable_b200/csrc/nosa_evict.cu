@@ -185,15 +185,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
         move16(d, s, rows * (kRowBytes / 16));
         move16(d + kHalfBlockBytes, s + kHalfBlockBytes, rows * (kRowBytes / 16));
     } else if (local) {
-        const uint8_t *s = p.kv8.tail + (int64_t)u * kBlockBytes;
-        uint8_t *d = p.dst_kv8.tail + (int64_t)u * kBlockBytes;
+        const uint8_t *s = p.tail + (int64_t)u * kBlockBytes;
+        uint8_t *d = p.dst_tail + (int64_t)u * kBlockBytes;
         move16(d, s, rows * (kRowBytes / 16));
         move16(d + kHalfBlockBytes, s + kHalfBlockBytes, rows * (kRowBytes / 16));
     } else {
-        move16(p.dst_store + db * kBlock8Bytes, p.store + sb * kBlock8Bytes, kBlock8Bytes / 16);
-        if (tid == 0)
-            p.dst_kv8.scales[(int64_t)u * p.dst_kv8.scale_stride + i] =
-                p.kv8.scales[(int64_t)u * p.kv8.scale_stride + b];
+        move16(p.dst_store + db * kRec8Bytes, p.store + sb * kRec8Bytes, kHeld8Bytes / 16);
     }
     const int ck_bytes = kD * (p.ck_bf16 ? 2 : 4);  // one pooled key
     move16(p.dst_ck + db * kSubPerBlock * ck_bytes, p.ck + sb * kSubPerBlock * ck_bytes, rows / kSub * (ck_bytes / 16));

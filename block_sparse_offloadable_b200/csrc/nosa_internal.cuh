@@ -11,14 +11,9 @@ namespace nosa {
 // How the blocks of a KV store are held (the NOSA_FLAG_KV_* bits).
 constexpr int kFmtBf16 = 0, kFmtInt8 = 1, kFmtE4m3 = 2;
 
-// The 8-bit store besides its blocks of codes, in device memory: the scales of each block's keys and
-// values, and the newest block of each unit in bf16.  A unit's row of scales is scale_stride blocks
-// (an even number: 16-byte aligned).
-struct Kv8 {
-    float2 *scales;        // [u][scale_stride] (s_K, s_V)
-    uint8_t *tail;         // [u][2][64][D] bf16
-    int32_t scale_stride;
-};
+// The 8-bit store: a record per block (kRec8Bytes apart) with the codes of its keys and values,
+// [2][64][D] bytes, then its 64 eviction logits, s_K and s_V (fp32); and per unit, in device memory, a
+// tail: the newest block in bf16, [2][64][D].
 
 struct AppendParams {
     const uint16_t *k_new;   // [u][T][D]
@@ -42,8 +37,8 @@ struct AppendParams {
     int32_t *pool;           // [u][nblk] fill reading: not-dropped candidates by E rank
     int32_t *pool_n;         // [u]
     int32_t nblk, nsub, nslots, units, heads_kv, k_e, offload, T, ck_bf16, fill;
-    int32_t fmt;             // kFmt*; not kFmtBf16: store and cache hold blocks of codes
-    Kv8 kv8;
+    int32_t fmt;             // kFmt*; not kFmtBf16: store and cache hold records of codes
+    uint8_t *tail;           // [u][2][64][D] bf16, 8-bit store
 };
 
 struct SelectParams {
@@ -81,7 +76,7 @@ struct CacheParams {
     uint32_t *miss_list;      // [u][max_sel] workspace: (slot << 20 | block) of each block to fetch
     uint32_t *err;
     int32_t nblk, nslots, units, max_sel;
-    int32_t fmt;              // kFmt*: 32 or 16 KiB a block
+    int32_t fmt;              // kFmt*: 32 KiB a block, or a record
 };
 
 struct EvictParams {
@@ -90,7 +85,8 @@ struct EvictParams {
     const uint8_t *store, *ck;
     const float *e;
     const double *blk_evict;
-    Kv8 kv8, dst_kv8;
+    const uint8_t *tail;       // 8-bit store
+    uint8_t *dst_tail;
     int32_t *kept;             // [u][keep + 1] old numbers, ascending, -1 padded
     float *dst_weights;        // [u][dst_nblk]
     int32_t *dst_seq_len, *dst_gamma_e, *dst_gamma_n, *dst_pool, *dst_pool_n;
@@ -133,12 +129,12 @@ struct DecodeParams {
     uint32_t *res_bits;         // [u][bits_words] membership of Gamma_e + local (same)
     int32_t k_e, k_q, nblk, bits_words;
     int32_t fmt;                // kFmt* of the blocks
-    Kv8 kv8;
+    const uint8_t *records;     // 8-bit store: the buffer of records (blocks_per_unit per unit)
     float *weights;             // [u][nblk] or null: each attended block's weight is added
-    float *rec;                 // with weights: [items][4 warps][8 heads] log2 of each warp's sum of 2^x
+    float *rec;                 // with weights: [items][8 heads] log2 of the item's sum of 2^x
 };
 
-constexpr int kRecFloats = 32;  // one item's weights
+constexpr int kRecFloats = kMaxG;  // one item's weights
 constexpr int kPartFloats = 2 * kMaxG + kMaxG * kD;  // m[8], l[8], o[8][128]
 
 // The fused step (nosa_fused_step): append + select + sparse decode of a device-resident store in
@@ -165,7 +161,8 @@ struct StepParams {
 int launch_append(const AppendParams &p, cudaStream_t stream);
 int launch_select(const SelectParams &p, cudaStream_t stream);
 int launch_cache_sync(const CacheParams &p, cudaStream_t stream);
-int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream);
+int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, cudaStream_t stream);
+int launch_decode_items(const DecodeParams &p, const CUtensorMap &tmap, const CUtensorMap &tail_map, cudaStream_t stream);
 int launch_evict(const EvictParams &p, cudaStream_t stream);
 int launch_step(const StepParams &p, const CUtensorMap &tmap, cudaStream_t stream);
 

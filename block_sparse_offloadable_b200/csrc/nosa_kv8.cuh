@@ -57,10 +57,11 @@ __device__ __forceinline__ uint2 code8(const uint4 &v, float r, int fmt) {
     return make_uint2(code4(v.x, v.y, r, fmt), code4(v.z, v.w, r, fmt));
 }
 
-// Code the block in `tail` (64 key rows, 64 value rows, bf16) into dst, by one warp: its scales to
-// *sc.  Twice over the 32 KiB, which the L2 holds; eight loads in flight.
-__device__ __forceinline__ void code_tail(const uint8_t *tail, uint8_t *dst, float2 *sc, int lane, int fmt) {
+// Code the block in `tail` (64 key rows, 64 value rows, bf16), whose logits are e, into the record
+// dst, by one warp.  Twice over the 32 KiB, which the L2 holds; eight loads in flight.
+__device__ __forceinline__ void code_tail(const uint8_t *tail, const float *e, uint8_t *dst, int lane, int fmt) {
     constexpr int kPer = kHalfBlockBytes / 16 / 32;  // 16-byte pieces per lane and half
+    float *side = reinterpret_cast<float *>(dst + kBlock8Bytes);
     float2 s[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -77,7 +78,9 @@ __device__ __forceinline__ void code_tail(const uint8_t *tail, uint8_t *dst, flo
 #pragma unroll 8
         for (int i = 0; i < kPer; ++i) to[32 * i] = code8(src[32 * i], s[half].y, fmt);
     }
-    if (lane == 0) *sc = make_float2(s[0].x, s[1].x);
+    side[lane] = e[lane];
+    side[lane + 32] = e[lane + 32];
+    if (lane < 2) side[kBlock + lane] = lane ? s[1].x : s[0].x;
 }
 
 }  // namespace nosa

@@ -118,7 +118,7 @@ typedef struct nosa_config {
  * over the block gives NaN.  The newest (local) block of a unit is held in bf16 in the unit's tail,
  * and coded once, when the first token of the next block arrives.  Pooled keys and eviction scores
  * are those of the bf16 input.  Every call works with these flags but nosa_fused_step
- * (NOSA_ERR_UNSUPPORTED); a missed block is 16 KiB to fetch, not 32.
+ * (NOSA_ERR_UNSUPPORTED); a missed block is 16656 bytes to fetch, not 32768.
  */
 #define NOSA_FLAG_KV_INT8 0x8
 #define NOSA_FLAG_KV_E4M3 0x10
@@ -129,10 +129,11 @@ typedef struct nosa_config {
  * nslots = k_q + k_e + 2):
  *   kv_store    bf16 [u][nblk][2][64][D]; [..][0] = keys, [..][1] = values.
  *               Device memory if offload == 0, host memory if offload == 1.
- *               With NOSA_FLAG_KV_INT8 / _E4M3: codes [u][nblk][2][64][D], one byte each, and,
- *               in the same buffer where it is device memory (offload == 0), behind them (n2 = nblk
- *               rounded up to an even number): scales fp32 [u][n2][2] (keys, values), padded
- *               to a multiple of 256 bytes, then tails bf16 [u][2][64][D].
+ *               With NOSA_FLAG_KV_INT8 / _E4M3: a record of 16768 bytes per block, [u][nblk]: codes
+ *               [2][64][D], one byte each, then fp32 the block's 64 eviction logits and the scales
+ *               of its keys and of its values, and 120 bytes unused.  Behind the records, in the buffer that
+ *               is device memory (here if offload == 0), from the next multiple of 256 bytes
+ *               on: the tails, bf16 [u][2][64][D]
  *   evict_logit fp32 [u][max_ctx]   per-token eviction logit e_j (device)
  *   ck          fp32 [u][nsub][D]   compressed keys: mean of each 16-token sub-block (device);
  *               bf16 [u][nsub][D] with NOSA_FLAG_CK_BF16
@@ -142,8 +143,7 @@ typedef struct nosa_config {
  *   gamma_n     int32 [u]           |Gamma_e| (device)
  *   seq_len     int32 [u]           tokens held, L (device)
  *   cache       bf16 [u][nslots][2][64][D]  offload block cache (device; NULL if offload == 0)
- *               with NOSA_FLAG_KV_INT8 / _E4M3: codes [u][nslots][2][64][D], then the scales
- *               (of every block, resident or not) and tails as above
+ *               with NOSA_FLAG_KV_INT8 / _E4M3: records [u][nslots], then the tails, as above
  *   slot_block  int32 [u][nslots]   block held by each cache slot, -1 = free (device; offload only)
  *   block_slot  int32 [u][nblk]     cache slot of each block, -1 = not resident (device; offload only)
  *   err         uint32 [1]          device error word (device)

@@ -78,7 +78,7 @@ def test_decode_from_empty_over_block_borders(fmt, offload, how):
     else:  # the resident blocks hold the codes; so does host memory
         torch.cuda.synchronize()
         codes = lay.kv8_views()[0].cpu()
-        host = lay.kv_store.view(codes.dtype).view(t.units, -1, 2, 64, 128)
+        host = lay.kv_store.view(codes.dtype).view(t.units, -1, nosa.RECORD_BYTES)[:, :, :16384].unflatten(2, (2, 64, 128))
         bt = lay.block_table.cpu().numpy()
         for u, s in enumerate(H.sels(lay)):
             for j, b in enumerate(s):
@@ -92,7 +92,7 @@ def test_decode_from_empty_over_block_borders(fmt, offload, how):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("B,Hq,Hkv,lens", [
     (1, 1, 1, [1]), (1, 8, 1, [64]), (1, 3, 1, [65]), (2, 10, 2, [128, 129]), (3, 7, 1, [0, 1000, 63]),
-    (1, 16, 2, [64 * 70 + 1]), (5, 16, 16, [200, 64, 65, 0, 511]), (40, 16, 4, [65 + 7 * i for i in range(40)])])
+    (1, 16, 2, [64 * 70 + 1]), (24, 8, 2, [64 * 60 - 100 * i for i in range(24)]), (5, 16, 16, [200, 64, 65, 0, 511]), (40, 16, 4, [65 + 7 * i for i in range(40)])])
 def test_dense(fmt, B, Hq, Hkv, lens):
     T = max(lens)
     t = H.Tokens(B, Hq, Hkv, T, seed=B + T)

@@ -26,7 +26,7 @@ def check_weights(t, got, before, q, units, blocks, nblk):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("B,Hq,Hkv,lens", [(1, 1, 1, [1]), (1, 8, 1, [65]), (3, 7, 1, [0, 1000, 63]),
-                                           (1, 10, 2, [64 * 70 + 1]), (1, 16, 2, [64 * 300]),
+                                           (1, 10, 2, [64 * 70 + 1]), (24, 8, 2, [64 * 60 - 100 * i for i in range(24)]), (1, 16, 2, [64 * 300]),
                                            (40, 16, 4, [65 + 7 * i for i in range(40)])])
 def test_dense_weights(fmt, B, Hq, Hkv, lens):
     T = max(lens)

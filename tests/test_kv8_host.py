@@ -28,13 +28,13 @@ def test_flags(fmt):
 @pytest.mark.parametrize("max_ctx", [64, 192, 8192])
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_sizes(fmt, max_ctx):
-    u, nblk, slots = 4, max_ctx // 64, 16 + 48 + 2
-    side = (u * (nblk + nblk % 2) * 8 + 255) // 256 * 256 + u * 32768  # scales, then bf16 tails
+    u, nblk, slots, rec = 4, max_ctx // 64, 16 + 48 + 2, 16768  # 16384 codes, 66 floats, padded to lines of 128
     dev, off = cfg(kv_format=fmt, max_ctx=max_ctx), cfg(kv_format=fmt, max_ctx=max_ctx, offload=True)
-    assert nosa.nosa_state_bytes(dev, nosa.BUF_KV_STORE) == u * nblk * 16384 + side
+    whole = lambda n: (u * n * rec + 255) // 256 * 256 + u * 32768  # noqa: E731  records, then bf16 tails
+    assert nosa.nosa_state_bytes(dev, nosa.BUF_KV_STORE) == whole(nblk)
     assert nosa.nosa_state_bytes(dev, nosa.BUF_CACHE) == 0
-    assert nosa.nosa_state_bytes(off, nosa.BUF_KV_STORE) == u * nblk * 16384
-    assert nosa.nosa_state_bytes(off, nosa.BUF_CACHE) == u * slots * 16384 + side
+    assert nosa.nosa_state_bytes(off, nosa.BUF_KV_STORE) == u * nblk * rec
+    assert nosa.nosa_state_bytes(off, nosa.BUF_CACHE) == whole(slots)
     for c in (dev, off):  # the pooled keys and the other state do not change
         assert nosa.nosa_state_bytes(c, nosa.BUF_CK) == u * (max_ctx // 16) * 128 * 4
     assert nosa.nosa_workspace_bytes(dev, nosa.WS_FUSED_STEP) == 0
@@ -45,8 +45,8 @@ def test_sizes(fmt, max_ctx):
 def test_weights_workspaces():
     c = cfg()
     base = 256 + (148 * 2 * (2 * 8 + 8 * 128) * 4 + 255) // 256 * 256
-    assert nosa.nosa_workspace_bytes(c, nosa.WS_SPARSE_WEIGHTS) == base + 4 * 65 * 128
-    assert nosa.nosa_workspace_bytes(c, nosa.WS_DENSE_WEIGHTS) == base + 4 * 128 * 128
+    assert nosa.nosa_workspace_bytes(c, nosa.WS_SPARSE_WEIGHTS) == base + 4 * 65 * 32
+    assert nosa.nosa_workspace_bytes(c, nosa.WS_DENSE_WEIGHTS) == base + 4 * 128 * 32
     assert nosa.nosa_workspace_bytes(cfg(offload=True), nosa.WS_DENSE_WEIGHTS) == 0
 
 
