@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libnosa.so")
 _SOURCES = ["nosa_api.cu", "nosa_append.cu", "nosa_select.cu", "nosa_cache.cu", "nosa_decode.cu", "nosa_step.cu",
             "nosa_noalloc.cu", "nosa_diag.cu", "nosa_evict.cu", "nosa_decode_items.cu"]
 _HEADERS = ["nosa_common.cuh", "nosa_internal.cuh", "nosa_append_unit.cuh", "nosa_attend.cuh", "nosa_attend8.cuh",
-            "nosa_kv8.cuh", "nosa_decode_work.cuh"]
+            "nosa_kv8.cuh", "nosa_decode_work.cuh", "nosa_topk.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
 
@@ -131,7 +131,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
+    if stream is None:  # the current device's current stream, without the Stream object (3 us of host time)
+        if torch.cuda.is_initialized():
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -335,6 +337,15 @@ class NosaLayer:
         self.ws_cache = ws(WS_CACHE_SYNC)
         self.split = None if cfg.flags & FLAG_FILL else ws(WS_SPLIT)
         self.ws_step = ws(WS_FUSED_STEP)
+        self._kv8 = None
+        if cfg.flags & (FLAG_KV_INT8 | FLAG_KV_E4M3):
+            buf = self.cache if cfg.offload else self.kv_store
+            n = cfg.k_q + cfg.k_e + 2 if cfg.offload else cfg.max_ctx // cfg.block
+            dtype = torch.int8 if cfg.flags & FLAG_KV_INT8 else torch.float8_e4m3fn
+            r, tail = RECORD_BYTES, (self.units * n * RECORD_BYTES + 255) // 256 * 256
+            self._kv8 = (buf.view(dtype).as_strided((self.units, n, 2, 64, 128), (n * r, r, 8192, 128, 1)),
+                         buf.view(torch.float32).as_strided((self.units, n, 2), (n * r // 4, r // 4, 1), 4096 + 64),
+                         buf[tail:tail + self.units * 32768].view(torch.bfloat16).view(self.units, 2, 64, 128))
         self.weights = self.ws_sparse_weights = self.ws_dense_weights = None
         if weights:
             self.weights = torch.zeros((self.units, cfg.max_ctx // cfg.block), dtype=torch.float32, device=dev)
@@ -407,16 +418,9 @@ class NosaLayer:
     def kv8_views(self):
         """Views of an 8-bit layer's buffer: codes (int8 or float8_e4m3fn [units][blocks][2][64][D]), scales fp32
         [units][blocks][2] and bf16 tails [units][2][64][D].  With offload the blocks are the cache's slots."""
-        cfg = self.cfg
-        if not cfg.flags & (FLAG_KV_INT8 | FLAG_KV_E4M3):
+        if self._kv8 is None:
             raise ValueError("kv8_views: the layer's KV store is bf16")
-        buf = self.cache if cfg.offload else self.kv_store
-        n = cfg.k_q + cfg.k_e + 2 if cfg.offload else cfg.max_ctx // cfg.block
-        dtype = torch.int8 if cfg.flags & FLAG_KV_INT8 else torch.float8_e4m3fn
-        r, tail = RECORD_BYTES, (self.units * n * RECORD_BYTES + 255) // 256 * 256
-        return (buf.view(dtype).as_strided((self.units, n, 2, 64, 128), (n * r, r, 8192, 128, 1)),
-                buf.view(torch.float32).as_strided((self.units, n, 2), (n * r // 4, r // 4, 1), 4096 + 64),
-                buf[tail:tail + self.units * 32768].view(torch.bfloat16).view(self.units, 2, 64, 128))
+        return self._kv8
 
     def decode_step(self, k_new, v_new, e_new, q, out, stream=None):
         """One decode step of this layer into `out` (bf16 bits [B][Hq][D]): with the KV store in

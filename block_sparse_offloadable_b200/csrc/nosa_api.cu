@@ -369,11 +369,8 @@ int nosa_state_init(const nosa_config *c, const nosa_state *st, void *stream) {
     uint8_t *s;
     if ((rc = store_addr(c, st, &s))) return rc;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    bool ok = cudaMemsetAsync(st->gamma_n, 0, nosa_state_bytes(c, NOSA_BUF_GAMMA_N), cs) == cudaSuccess &&
-              cudaMemsetAsync(st->seq_len, 0, nosa_state_bytes(c, NOSA_BUF_SEQ_LEN), cs) == cudaSuccess &&
-              cudaMemsetAsync(st->err, 0, sizeof(uint32_t), cs) == cudaSuccess;
-    if (ok && (c->flags & NOSA_FLAG_FILL))
-        ok = cudaMemsetAsync(st->pool_n, 0, nosa_state_bytes(c, NOSA_BUF_POOL_N), cs) == cudaSuccess;
+    bool ok = launch_init(st->gamma_n, st->seq_len, (c->flags & NOSA_FLAG_FILL) ? st->pool_n : nullptr, st->err,
+                          c->batch * c->heads_kv, cs) == NOSA_OK;
     if (ok && c->offload) {
         ok = cudaMemsetAsync(st->slot_block, 0xFF, nosa_state_bytes(c, NOSA_BUF_SLOT_BLOCK), cs) == cudaSuccess &&
              cudaMemsetAsync(st->block_slot, 0xFF, nosa_state_bytes(c, NOSA_BUF_BLOCK_SLOT), cs) == cudaSuccess &&

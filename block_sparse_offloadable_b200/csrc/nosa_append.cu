@@ -12,6 +12,7 @@
 // and one 256 B read of the eviction logits when a block completes, so the
 // kernel is latency-bound by design.
 #include "nosa_append_unit.cuh"
+#include "nosa_topk.cuh"
 
 namespace nosa {
 
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(256) prefill_store8_kernel(const AppendParams 
     __shared__ __align__(16) uint8_t ks[kHalfBlockBytes];
     __shared__ uint32_t s_max[2][8];
     __shared__ float s_e[kBlock];
+    pdl_trigger();  // Gamma_e's CTAs are few and wait for this grid
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t bpu = (p.T + kBlock - 1) / kBlock;
     const int32_t u = (int32_t)(blockIdx.x / bpu), blk = (int32_t)(blockIdx.x % bpu);
@@ -351,68 +353,62 @@ __global__ void __launch_bounds__(256) prefill_head_kernel(const AppendParams p)
     }
 }
 
+// An integer key in the order of E: -0 as +0, NaN above every number.
+__device__ __forceinline__ uint64_t evict_key(double e) {
+    if (e != e) return ~0ull - 1;
+    const uint64_t x = (uint64_t)__double_as_longlong(e == 0.0 ? 0.0 : e);
+    return (x >> 63) ? ~x : (x | (1ull << 63));
+}
+
 // Gamma_e := top-k_e of the candidates by E (ties to the lower block), ascending;
 // fill reading: also the pool of every candidate in rank order (nothing is
-// dropped before the first decode step).  One CTA per unit; rank counting over
-// the candidates held in shared memory (the ranks are a permutation).
-__global__ void __launch_bounds__(256) prefill_gamma_kernel(const AppendParams p) {
+// dropped before the first decode step).  One CTA per unit, the candidates' keys
+// in shared memory: radix selection, and for the pool rank counting (the ranks
+// are a permutation).
+__global__ void __launch_bounds__(kTopThreads) prefill_gamma_kernel(const AppendParams p) {
+    pdl_wait();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t s_max[2][8];
-    const int32_t u = blockIdx.x;
+    __shared__ TopShared top;
+    const int32_t u = blockIdx.x, tid = threadIdx.x;
     if (p.seq_len[u] != 0) {
-        if (threadIdx.x == 0) set_error(p.err, NOSA_EFLAG_STATE);
+        if (tid == 0) set_error(p.err, NOSA_EFLAG_STATE);
         return;
     }
     const int32_t len = unit_len(p, u);
     const int32_t nb_c = len > 0 ? (len - 1) / kBlock : 0;
-    double *E = reinterpret_cast<double *>(smem);
-    uint8_t *flag = smem + (size_t)p.nblk * sizeof(double);
-    for (int i = threadIdx.x; i < nb_c; i += blockDim.x) E[i] = p.blk_evict[(int64_t)u * p.nblk + i];
+    uint64_t *keys = reinterpret_cast<uint64_t *>(smem);
+    for (int i = tid; i < nb_c; i += kTopThreads) keys[i] = evict_key(p.blk_evict[(int64_t)u * p.nblk + i]);
     __syncthreads();
-    const bool pool = p.fill && p.k_e > 0;
-    const int32_t stop = pool ? nb_c : p.k_e;
-    for (int i = threadIdx.x; i < nb_c; i += blockDim.x) {
-        const double ei = E[i];
-        int32_t rank = 0;
-        for (int j = 0; j < nb_c && rank < stop; ++j) {
-            const double ej = E[j];
-            rank += (ej > ei) || (ej == ei && j < i);
+    if (p.fill && p.k_e > 0) {
+        for (int i = tid; i < nb_c; i += kTopThreads) {
+            const uint64_t ki = keys[i];
+            int32_t rank = 0;
+            for (int j = 0; j < nb_c; ++j) rank += keys[j] > ki || (keys[j] == ki && j < i);
+            p.pool[(int64_t)u * p.nblk + rank] = i;
         }
-        flag[i] = rank < p.k_e;
-        if (pool) p.pool[(int64_t)u * p.nblk + rank] = i;
+        if (tid == 0) p.pool_n[u] = nb_c;
+        __syncthreads();
     }
-    if (pool && threadIdx.x == 0) p.pool_n[u] = nb_c;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        const int32_t per = (nb_c + 31) / 32;
-        const int32_t b0 = min(lane * per, nb_c), b1 = min(b0 + per, nb_c);
-        int32_t cnt = 0;
-        for (int i = b0; i < b1; ++i) cnt += flag[i];
-        int32_t pre = cnt;
-        for (int o = 1; o < 32; o <<= 1) {
-            int32_t v = __shfl_up_sync(0xFFFFFFFFu, pre, o);
-            if (lane >= o) pre += v;
+    const int32_t n = number_chosen(keys, nb_c, nb_c <= p.k_e, p.k_e, top);
+    int32_t *ge = p.gamma_e + (int64_t)u * p.k_e;
+    for (int i = tid; i < nb_c; i += kTopThreads) {
+        const int32_t at = (int32_t)keys[i];
+        if (at < 0) continue;
+        if (p.offload) {  // Gamma_e starts resident: slot 1 + its place in the ascending list
+            p.slot_block[(int64_t)u * p.nslots + 1 + at] = i;
+            p.block_slot[(int64_t)u * p.nblk + i] = 1 + at;
         }
-        int32_t at = pre - cnt;
-        int32_t *ge = p.gamma_e + (int64_t)u * p.k_e;
-        for (int i = b0; i < b1; ++i)
-            if (flag[i]) {
-                if (p.offload) {  // Gamma_e starts resident: slot 1 + its place in the ascending list
-                    p.slot_block[(int64_t)u * p.nslots + 1 + at] = i;
-                    p.block_slot[(int64_t)u * p.nblk + i] = 1 + at;
-                }
-                ge[at++] = i;
-            }
-        if (lane == 31) {
-            p.gamma_n[u] = pre;
-            if (p.offload && len > 0) {
-                const int32_t local = (len - 1) / kBlock;
-                p.slot_block[(int64_t)u * p.nslots] = local;
-                p.block_slot[(int64_t)u * p.nblk + local] = 0;
-            }
-            p.seq_len[u] = len;
+        ge[at] = i;
+    }
+    if (tid == 0) {
+        p.gamma_n[u] = n;
+        if (p.offload && len > 0) {
+            const int32_t local = (len - 1) / kBlock;
+            p.slot_block[(int64_t)u * p.nslots] = local;
+            p.block_slot[(int64_t)u * p.nblk + local] = 0;
         }
+        p.seq_len[u] = len;
     }
     if (p.offload) {
         // copy the Gamma_e blocks from the prefill input (on the device) into their
@@ -452,6 +448,22 @@ __global__ void __launch_bounds__(256) prefill_gamma_kernel(const AppendParams p
     }
 }
 
+// Empty sequences: what a unit holds one of, in one launch (a memset each took longer).
+__global__ void __launch_bounds__(256) init_kernel(int32_t *gamma_n, int32_t *seq_len, int32_t *pool_n, uint32_t *err,
+                                                   int32_t units) {
+    const int u = blockIdx.x * blockDim.x + threadIdx.x;
+    if (u == 0) *err = 0;
+    if (u >= units) return;
+    gamma_n[u] = 0;
+    seq_len[u] = 0;
+    if (pool_n) pool_n[u] = 0;
+}
+
+int launch_init(int32_t *gamma_n, int32_t *seq_len, int32_t *pool_n, uint32_t *err, int32_t units, cudaStream_t stream) {
+    init_kernel<<<(units + 255) / 256, 256, 0, stream>>>(gamma_n, seq_len, pool_n, err, units);
+    return cudaGetLastError() == cudaSuccess ? NOSA_OK : NOSA_ERR_CUDA;
+}
+
 int launch_append(const AppendParams &p, cudaStream_t stream) {
     if (p.T == 1 && p.w1) {
         if (cudaFuncSetAttribute(append_head_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -488,14 +500,16 @@ int launch_append(const AppendParams &p, cudaStream_t stream) {
         if (g > 148 * 16) g = 148 * 16;
         prefill_pool_kernel<<<(unsigned)g, 256, 0, stream>>>(p);
     }
-    const size_t smem = (size_t)p.nblk * (sizeof(double) + 1);
+    const size_t smem = (size_t)p.nblk * sizeof(uint64_t);
     if (smem > 48 * 1024) {
         if (cudaFuncSetAttribute(prefill_gamma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
             return NOSA_ERR_CUDA;
     }
-    prefill_gamma_kernel<<<p.units, 256, smem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? NOSA_OK : NOSA_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return NOSA_ERR_CUDA;
+    return launch_pdl(prefill_gamma_kernel, dim3(p.units), dim3(kTopThreads), smem, stream, p) == cudaSuccess
+               ? NOSA_OK
+               : NOSA_ERR_CUDA;
 }
 
 }  // namespace nosa

@@ -247,14 +247,9 @@ __device__ __forceinline__ void store_partial(float *part, int h, int d, float M
 
 // kNan: a denominator that is NaN (a block whose scale is NaN) gives NaN, not zero.
 template <bool kNan = false>
-__device__ __forceinline__ bool has_weight(float ls) {
-    return kNan ? ls != 0.f : ls > 0.f;
-}
-
-template <bool kNan = false>
 __device__ __forceinline__ uint2 pack_out4(float4 acc, float ls) {
     uint2 pk;
-    if (has_weight<kNan>(ls)) {
+    if (kNan ? ls != 0.f : ls > 0.f) {
         pk.x = pack_bf16x2(acc.x / ls, acc.y / ls);
         pk.y = pack_bf16x2(acc.z / ls, acc.w / ls);
     } else {
@@ -266,15 +261,15 @@ __device__ __forceinline__ uint2 pack_out4(float4 acc, float ls) {
 // The last of C <= kOnePassPieces pieces of a unit merges their partial records, piece t at
 // src0 + t * stride, in piece order, in one pass: each consumer thread takes 4 dims of one head
 // and issues its loads at once (all of them with at most kAtOnce pieces: one round trip; more
-// registers).  Writes bf16 out, and where s_lse is given the log2 of each head's whole sum there.
-template <int kAtOnce = kFewPieces, bool kNan = false, int kThreads = kConsThreads>
+// registers).  Writes bf16 out.
+template <int kAtOnce = kFewPieces>
 __device__ __forceinline__ void merge_pieces_onepass(const float *src0, int64_t stride, int C, int G, uint16_t *out,
-                                                     int ctid, float *s_lse = nullptr) {
+                                                     int ctid) {
     static_assert(kAtOnce <= kOnePassPieces, "at most kOnePassPieces pieces");
-    for (int v = ctid; v < G * (kD / 4); v += kThreads) {
+    for (int v = ctid; v < G * (kD / 4); v += kConsThreads) {
         const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
         float mt[kOnePassPieces];
-        float ls = 0.f, M = kNegInf;
+        float ls = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (C <= kAtOnce) {
             // few pieces: every load at once, one round trip
@@ -288,6 +283,7 @@ __device__ __forceinline__ void merge_pieces_onepass(const float *src0, int64_t 
                 ot[t] = t < C ? __ldcg(reinterpret_cast<const float4 *>(st_t + 2 * kMaxG + h * kD + d4))
                               : make_float4(0.f, 0.f, 0.f, 0.f);
             }
+            float M = kNegInf;
 #pragma unroll
             for (int t = 0; t < kAtOnce; ++t) M = fmaxf(M, mt[t]);
 #pragma unroll
@@ -302,6 +298,7 @@ __device__ __forceinline__ void merge_pieces_onepass(const float *src0, int64_t 
         } else {
 #pragma unroll
             for (int t = 0; t < kOnePassPieces; ++t) mt[t] = t < C ? __ldcg(src0 + (int64_t)t * stride + h) : kNegInf;
+            float M = kNegInf;
 #pragma unroll
             for (int t = 0; t < kOnePassPieces; ++t) M = fmaxf(M, mt[t]);
 #pragma unroll
@@ -316,8 +313,7 @@ __device__ __forceinline__ void merge_pieces_onepass(const float *src0, int64_t 
                 }
             }
         }
-        *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<kNan>(acc, ls);
-        if (s_lse && d4 == 0) s_lse[h] = M + log2f(ls);
+        *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4(acc, ls);
     }
 }
 
@@ -340,12 +336,11 @@ __device__ __forceinline__ MergeScratch merge_scratch(float *scratch, int nc) {
     return m;
 }
 
-// kNan as in has_weight.  One warp per head finds the weights, then each consumer thread combines 4 dims of one head.
+// One warp per head finds the weights, then each consumer thread combines 4 dims of one head.
 // res == nullptr: writes the bf16 output; otherwise the merged record (the split decode's state).
-template <bool kNan = false, int kThreads = kConsThreads>
 __device__ __forceinline__ void merge_general(const MergeScratch &ms, int nc, int G, uint16_t *out, float *res,
                                              int warp, int lane, int ctid) {
-    for (int h = warp; h < G; h += kThreads / 32) {
+    for (int h = warp; h < G; h += kConsWarps) {
         float M = kNegInf;
         for (int t = lane; t < nc; t += 32) M = fmaxf(M, __ldcg(ms.src[t] + h));
 #pragma unroll
@@ -364,8 +359,8 @@ __device__ __forceinline__ void merge_general(const MergeScratch &ms, int nc, in
             ms.Ms[h] = M;
         }
     }
-    consumer_sync<kThreads>();
-    for (int v = ctid; v < G * (kD / 4); v += kThreads) {  // 4 dims per thread
+    consumer_sync();
+    for (int v = ctid; v < G * (kD / 4); v += kConsThreads) {  // 4 dims per thread
         const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -384,7 +379,7 @@ __device__ __forceinline__ void merge_general(const MergeScratch &ms, int nc, in
             }
             continue;
         }
-        *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<kNan>(acc, ls);
+        *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4(acc, ls);
     }
 }
 

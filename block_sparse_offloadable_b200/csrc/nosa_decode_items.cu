@@ -125,23 +125,97 @@ __device__ __forceinline__ void merge_resident4(const DecodeParams &p, int32_t u
     merge_resident(p, u, h, d4 + 3, M, acc.w, lsum);
 }
 
-// Add each of a unit's blocks' weight: the items' values (rec, left by the warps that attended them)
-// against the whole sums' log2 per head.  By all consumer threads of the unit's last CTA.
-__device__ __forceinline__ void add_weights(const DecodeParams &p, int32_t u, int32_t item0, int32_t n,
-                                            const float *s_lse, int ctid) {
-    for (int32_t j = ctid; j < n; j += kItemConsThreads) {
-        int32_t lb, pb;
-        item_block(p, u, n - 1 - j, lb, pb);  // the items' order, see below
-        if (lb < 0 || (int64_t)lb * kBlock >= p.seq_len[u]) continue;
-        const float4 *rec = reinterpret_cast<const float4 *>(p.rec + (int64_t)(item0 + j) * kRecFloats);
-        const float4 a = __ldcg(rec), b = __ldcg(rec + 1);
-        const float v[kMaxG] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        float w = 0.f;
+// The last CTA of a unit merges the nc partial records src[], in order.  A thread takes 8 dims of a head and has the loads of kBatch records in flight at
+// once, since a round trip to the L2 (0.7 us) is what this costs.  Writes bf16 out, or the merged
+// record to res (the split decode's state); s_lse: the log2 of each head's whole sum.
+template <bool kNan>
+__device__ __forceinline__ void merge_records(const float *const *src, int nc, int G, uint16_t *out,
+                                           float *res, float *s_lse, int ctid) {
+    constexpr int kBatch = 4;
+#pragma unroll 1
+    for (int v = ctid; v < G * (kD / 8); v += kItemConsThreads) {
+        const int h = v / (kD / 8), d = (v % (kD / 8)) * 8;
+        float M = kNegInf, ls = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 1
+        for (int t0 = 0; t0 < nc; t0 += kBatch) {
+            float m[kBatch], l[kBatch];
+            float4 x[kBatch], y[kBatch];
 #pragma unroll
-        for (int h = 0; h < kMaxG; ++h)  // a head that sees nothing gives no weight
-            if (h < p.G && s_lse[h] != kNegInf) w += exp2f(v[h] - s_lse[h]);
-        atomicAdd(p.weights + (int64_t)u * p.nblk + lb, w);  // a caller's list may name a block twice
+            for (int t = 0; t < kBatch; ++t) {
+                m[t] = kNegInf;
+                if (t0 + t < nc) {
+                    const float *rec = src[t0 + t];
+                    const float4 *o = reinterpret_cast<const float4 *>(rec + 2 * kMaxG + h * kD + d);
+                    m[t] = __ldcg(rec + h);
+                    l[t] = __ldcg(rec + kMaxG + h);
+                    x[t] = __ldcg(o);
+                    y[t] = __ldcg(o + 1);
+                }
+            }
+            float Mn = M;
+#pragma unroll
+            for (int t = 0; t < kBatch; ++t) Mn = fmaxf(Mn, m[t]);
+            const float f0 = (M == kNegInf) ? 0.f : exp2f(M - Mn);
+            a.x *= f0; a.y *= f0; a.z *= f0; a.w *= f0;
+            b.x *= f0; b.y *= f0; b.z *= f0; b.w *= f0;
+            ls *= f0;
+#pragma unroll
+            for (int t = 0; t < kBatch; ++t)
+                if (t0 + t < nc) {
+                    const float f = (m[t] == kNegInf) ? 0.f : exp2f(m[t] - Mn);
+                    a.x = fmaf(f, x[t].x, a.x); a.y = fmaf(f, x[t].y, a.y);
+                    a.z = fmaf(f, x[t].z, a.z); a.w = fmaf(f, x[t].w, a.w);
+                    b.x = fmaf(f, y[t].x, b.x); b.y = fmaf(f, y[t].y, b.y);
+                    b.z = fmaf(f, y[t].z, b.z); b.w = fmaf(f, y[t].w, b.w);
+                    ls = fmaf(f, l[t], ls);
+                }
+            M = Mn;
+        }
+        if (res) {
+            *reinterpret_cast<float4 *>(res + 2 * kMaxG + h * kD + d) = a;
+            *reinterpret_cast<float4 *>(res + 2 * kMaxG + h * kD + d + 4) = b;
+            if (d == 0) {
+                res[h] = M;
+                res[kMaxG + h] = ls;
+            }
+        } else {
+            const uint2 lo = pack_out4<kNan>(a, ls), hi = pack_out4<kNan>(b, ls);
+            *reinterpret_cast<uint4 *>(out + h * kD + d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+        if (s_lse && d == 0) s_lse[h] = M + log2f(ls);
     }
+}
+
+// A block's weight: its item's values (left by the warp that attended it) against the log2 of the
+// whole sums per head.
+struct Weight {
+    int32_t lb;  // -1: none
+    float4 a, b;
+};
+
+__device__ __forceinline__ Weight load_weight(const DecodeParams &p, int32_t u, int32_t item0, int32_t n, int32_t j) {
+    Weight w;
+    int32_t pb;
+    w.lb = -1;
+    if (j >= n) return w;
+    const float4 *rec = reinterpret_cast<const float4 *>(p.rec + (int64_t)(item0 + j) * kRecFloats);
+    w.a = __ldcg(rec);
+    w.b = __ldcg(rec + 1);
+    const int32_t L = p.seq_len[u];
+    item_block(p, u, n - 1 - j, w.lb, pb);  // the items' order, see look_up
+    if ((int64_t)w.lb * kBlock >= L) w.lb = -1;
+    return w;
+}
+
+__device__ __forceinline__ void add_weight(const DecodeParams &p, int32_t u, const Weight &w, const float *s_lse) {
+    if (w.lb < 0) return;
+    const float v[kMaxG] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h)  // a head that sees nothing gives no weight
+        if (h < p.G && s_lse[h] != kNegInf) sum += exp2f(v[h] - s_lse[h]);
+    atomicAdd(p.weights + (int64_t)u * p.nblk + w.lb, sum);  // a caller's list may name a block twice
 }
 
 // An item: its unit, the unit's length, the block's number (-1: nothing) and its place in the buffer.
@@ -235,8 +309,9 @@ __global__ void __launch_bounds__(kItemThreads, 1)
     const auto first_item = [&](int32_t u) { return nominal ? u * p.max_sel : P[u]; };
     const auto unit_of = [&](int32_t x) { return nominal ? x / p.max_sel : find_unit(P, U, x); };
     const int32_t W = first_item(U);  // < 2^25
-    // Balanced: ranges over Ge CTAs, none with fewer items than consumer warps (but for the rest of
-    // the division) -- a CTA with one item costs a merge of its state and saves nothing.
+    // Balanced: ranges over Ge CTAs of no fewer items than consumer warps, where there are as many: a
+    // CTA with one item costs a merge of its state and saves nothing (65 blocks a unit, 2 units: 12.0 us
+    // with ranges of 5, 14.4 of 8 over 4 warps, 15.6 of 4).
     const int32_t C = p.pieces;
     const int32_t We = (W + kTakers - 1) / kTakers;
     const int32_t Ge = min(max(We, 1), grid);
@@ -360,10 +435,8 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             if (lane == warp && warp < n_items && by_consumer(mine, warp, nt)) issue(mine, warp, nt);
             __syncwarp();
         }
-        WarpState st;
-        st.reset();
         uint32_t qf[8][2];
-        [[maybe_unused]] Query8 q8;
+        [[maybe_unused]] Query8<k8 ? kFmt : kFmtE4m3> q8;
         int32_t L = 0;
         // a unit's queries (B fragments, dims permuted as the key loads) and length
         auto load_q = [&](int32_t uu) {
@@ -381,9 +454,11 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             L = p.seq_len[uu];
         };
         const int32_t first_unit = n_items > 0 ? unit_of(lo) : 0;
-        int32_t u = first_unit;
-        if (n_items > 0) load_unit(u);
+        int32_t u = first_unit, last_first = -1, last_other = -1;
         for (int32_t x = lo; x < hi;) {
+            load_unit(u);
+            WarpState st;
+            st.reset();
             const int32_t u_begin = first_item(u), u_end = first_item(u + 1);
             const int32_t seg_end = min(hi, u_end);
             const bool whole = x == u_begin && seg_end == u_end;
@@ -405,8 +480,8 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                                 attend16<Dims, kWeights>(st, qf, t, tails + tb * kHalfBlockBytes, e, lb, L, p.qk_log2,
                                                          r, c, sig, rec);
                             } else {
-                                attend8<kFmt, kWeights>(st, q8, t, e, e[kBlock], e[kBlock + 1], p.qk_log2, r, c, sig,
-                                                        rec);
+                                attend8<kWeights>(st, q8, p.q + (int64_t)u * p.G * kD, p.G, t, e, e[kBlock], e[kBlock + 1],
+                                                  p.qk_log2, r, c, sig, rec);
                             }
                         } else {
                             attend16<Dims, kWeights>(st, qf, t, t + kHalfBlockBytes, e, lb, L, p.qk_log2, r, c, sig,
@@ -422,7 +497,6 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             }
             const int32_t u_next = (seg_end < hi) ? unit_of(seg_end) : u;
             consumer_sync<kItemConsThreads>();
-            if (seg_end < hi) load_unit(u_next);  // in flight while the states are joined
             uint16_t *out = p.out + (int64_t)u * p.G * kD;
             float *part = p.part + ((int64_t)cta * 2 + slot) * kPartFloats;
             for (int v = ctid; v < p.G * (kD / 4); v += kItemConsThreads) {
@@ -443,51 +517,59 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                     }
                 }
             }
-            bool add = whole;  // this CTA ends the unit: it adds the weights
             consumer_sync<kItemConsThreads>();
             if (!whole) {
                 // hand-off: the partial is written (barrier), one thread counts it with release
                 // semantics; the unit's last contributor acquired the others' partials with the same
-                // atomic, and the barrier after it orders every thread's loads below after them
-                const int32_t cf = C > 0 ? u * C : cta_of(u_begin, W, Ge);
-                const int32_t cl = C > 0 ? u * C + C - 1 : cta_of((int64_t)u_end - 1, W, Ge);
-                if (ctid == 0) s_last = ((int32_t)atom_add_acq_rel_gpu(p.counter + u, 1u) == cl - cf);
+                // atomic, and the barrier after it orders every thread's later loads after them
+                const int32_t others = C > 0 ? C - 1 : cta_of((int64_t)u_end - 1, W, Ge) - cta_of(u_begin, W, Ge);
+                if (ctid == 0) s_last = (int32_t)atom_add_acq_rel_gpu(p.counter + u, 1u) == others;
                 consumer_sync<kItemConsThreads>();
-                add = s_last;
-                if (s_last && C > 0 && C <= kOnePassPieces) {
-                    // the C pieces' partials (piece t: slot 0 of CTA cf + t) in one pass
-                    if (ctid == 0) p.counter[u] = 0;
-                    merge_pieces_onepass<kFewPieces, k8, kItemConsThreads>(
-                        p.part + (int64_t)cf * 2 * kPartFloats, 2 * kPartFloats, C, p.G, out, ctid,
-                        kWeights ? s_lse : nullptr);
-                } else if (s_last) {
-                    if (ctid == 0) p.counter[u] = 0;
-                    // the CTA partials in CTA order (and, merging the rest pass, the resident state)
-                    const int nc = cl - cf + 1 + (p.mode == kModeRest ? 1 : 0);  // <= Ge + 1
-                    const MergeScratch ms = merge_scratch(scratch, nc);
-                    for (int t = ctid; t < nc; t += kItemConsThreads) {
-                        const int32_t cc = cf + t;
-                        if (cc > cl) {
-                            ms.src[t] = p.res_part + (int64_t)u * kPartFloats;
-                        } else {
-                            const int sl = (C > 0 || unit_of((int32_t)((int64_t)cc * W / Ge)) == u) ? 0 : 1;
-                            ms.src[t] = p.part + (int64_t)(cc * 2 + sl) * kPartFloats;
-                        }
-                    }
-                    consumer_sync<kItemConsThreads>();
-                    merge_general<k8, kItemConsThreads>(
-                        ms, nc, p.G, out, kResident ? p.res_part + (int64_t)u * kPartFloats : nullptr, warp, lane, ctid);
-                    if (kWeights && ctid < p.G) s_lse[ctid] = ms.Ms[ctid] + log2f(ms.lsum[ctid]);
-                }
-                consumer_sync<kItemConsThreads>();  // scratch and s_last are reused by the next segment
-            }
-            if (kWeights && add) {
-                add_weights(p, u, u_begin, u_end - u_begin, s_lse, ctid);
+                if (s_last) (slot == 0 ? last_first : last_other) = u;
+            } else if (kWeights) {
+                for (int32_t j = ctid; j < u_end - u_begin; j += kItemConsThreads)
+                    add_weight(p, u, load_weight(p, u, u_begin, u_end - u_begin, j), s_lse);
                 consumer_sync<kItemConsThreads>();
             }
-            st.reset();
             x = seg_end;
             u = u_next;
+        }
+        // The units whose last contributor this CTA is, at most its first and its last: merged here, after
+        // the stream, where the registers of the attention are free (a first unit's merge is rarely
+        // here: the CTA before it streams the rest of that unit at its end).
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int32_t um = k ? last_other : last_first;
+            if (um < 0) continue;
+            const int32_t u_begin = first_item(um), u_end = first_item(um + 1);
+            const int32_t cf = C > 0 ? um * C : cta_of(u_begin, W, Ge);
+            const int32_t cl = C > 0 ? um * C + C - 1 : cta_of((int64_t)u_end - 1, W, Ge);
+            if (ctid == 0) p.counter[um] = 0;
+            // the CTA partials in CTA order (and, merging the rest pass, the resident state)
+            const int nc = cl - cf + 1 + (p.mode == kModeRest ? 1 : 0);  // <= Ge + 1
+            const float **src = reinterpret_cast<const float **>(scratch);
+            for (int t = ctid; t < nc; t += kItemConsThreads) {
+                const int32_t cc = cf + t;
+                if (cc > cl) {
+                    src[t] = p.res_part + (int64_t)um * kPartFloats;
+                } else {
+                    const int sl = (C > 0 || unit_of((int32_t)((int64_t)cc * W / Ge)) == um) ? 0 : 1;
+                    src[t] = p.part + (int64_t)(cc * 2 + sl) * kPartFloats;
+                }
+            }
+            consumer_sync<kItemConsThreads>();
+            Weight w0;  // the first blocks' weights, in flight while the states are merged
+            if (kWeights) w0 = load_weight(p, um, u_begin, u_end - u_begin, ctid);
+            merge_records<k8>(src, nc, p.G, p.out + (int64_t)um * p.G * kD,
+                              kResident ? p.res_part + (int64_t)um * kPartFloats : nullptr, kWeights ? s_lse : nullptr,
+                              ctid);
+            consumer_sync<kItemConsThreads>();
+            if (kWeights) {
+                add_weight(p, um, w0, s_lse);
+                for (int32_t j = ctid + kItemConsThreads; j < u_end - u_begin; j += kItemConsThreads)
+                    add_weight(p, um, load_weight(p, um, u_begin, u_end - u_begin, j), s_lse);
+                consumer_sync<kItemConsThreads>();
+            }
         }
         // units without work, one CTA each: zero output (an empty state in the
         // resident pass; the resident state alone in the rest pass)

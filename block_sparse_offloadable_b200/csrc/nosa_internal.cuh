@@ -159,6 +159,7 @@ struct StepParams {
 };
 
 int launch_append(const AppendParams &p, cudaStream_t stream);
+int launch_init(int32_t *gamma_n, int32_t *seq_len, int32_t *pool_n, uint32_t *err, int32_t units, cudaStream_t stream);
 int launch_select(const SelectParams &p, cudaStream_t stream);
 int launch_cache_sync(const CacheParams &p, cudaStream_t stream);
 int launch_decode(const DecodeParams &p, const CUtensorMap &tmap, cudaStream_t stream);

@@ -78,7 +78,9 @@ class Unit:
         # instructions, each off by at most a step 2^-23 of what it has summed, two more roundings, the
         # logit's own and the reference maximum's): dz <= 2^-23 * 14 * (sum |q k| scale + |e|) <= 2^-19 of it.
         # P is rounded to f16 (2^-11 of it) over codes and to bf16 (2^-8) over bf16 rows, in the numerator
-        # and in the denominator; the output to bf16 (2^-8).  exp2 and the final sums: 2^-20.
+        # and in the denominator; the output to bf16 (2^-8).  exp2 and the final sums: 2^-20.  Over int8
+        # codes P is a multiple of 1/65535 of the block's largest weight: off by at most half of that,
+        # 2^-17 of the largest, for each of the block's tokens, whatever the token's own weight.
         fin = np.isfinite(e)
         mag = np.abs(q) @ np.abs(k).T * self.scale + np.where(fin, np.abs(np.where(fin, e, 0)), 0)[None]
         seen = p > 0
@@ -87,6 +89,10 @@ class Unit:
         dp = 2.0 ** -8 * (p * half).sum(1, keepdims=True) + 2.0 ** -11 * (p * ~half).sum(1, keepdims=True)
         tol = 2.0 ** -8 * np.abs(out) + 2 * (dp + dz + 2.0 ** -20) * (p @ np.abs(v)) + 1e-38
         at = np.searchsorted(blocks, rows // BLOCK)
+        if self.fmt == "int8":
+            top = np.zeros((self.G, len(blocks)))
+            np.maximum.at(top.T, at, np.where(half, 0, p).T)
+            tol += 2.0 ** -17 * top[:, at] @ np.abs(v)
         w, wt = np.zeros(len(blocks)), np.zeros(len(blocks))
         np.add.at(w, at, p.sum(0))
         np.add.at(wt, at, (p * (2 * dz + 2.0 ** -18)).sum(0))  # log2, exp2 and sums beside the logits' error
