@@ -57,6 +57,22 @@ WORKLOADS = {
 DEFAULT_WORKLOAD = "offload28-128k"
 
 
+def kv8(c):
+    """Whether the KV store holds its blocks in 8 bits."""
+    return c.get("kv_format", "bf16") != "bf16"
+
+
+def block_bytes(c):
+    """Bytes of one block of the KV store: keys and values in bf16, or a record (codes, logits, scales)."""
+    return 64 * D * 2 + 64 * 4 + 16 if kv8(c) else 64 * D * 2 * 2
+
+
+def attended_bytes(c, n):
+    """Bytes that attending n blocks of a unit reads, eviction logits included; the newest block is bf16."""
+    blk = 64 * D * 2 * 2 + 64 * 4
+    return (n - 1) * block_bytes(c) + blk if kv8(c) else n * blk
+
+
 def describe(c, groups):
     s = (f"{c['layers']} layers, batch {c['B']}, {c['Hq']} q / {c['Hkv']} kv heads, head_dim 128, "
          f"context {c['L']}, block 64, sub-block 16, k_q={c['k_q']}, k_e={c['k_e']}, local window 1 block, ")
@@ -69,11 +85,13 @@ def describe(c, groups):
         s += ", pooled keys stored bf16"
     if c.get("fill"):
         s += ", fill reading of the selection"
+    if kv8(c):
+        s += f", KV blocks held in {c['kv_format']} with a scale per block (the newest block in bf16)"
     if c.get("head"):
         s += ", eviction logits from the fused synthetic eviction head"
     if c.get("split"):
         s += ", decode split: Gamma_e + local attended while select and the cache sync run"
-    if c.get("step") and not (c["offload"] or c.get("fill") or c.get("head") or c.get("split")):
+    if c.get("step") and not (c["offload"] or c.get("fill") or c.get("head") or c.get("split") or kv8(c)):
         s += ", each layer's step (append, select, decode) in one launch"
     elif c.get("fuse"):
         s += ", append and select fused in one launch"
@@ -116,7 +134,8 @@ class Workload:
         self.n_steps = n_steps
         self.max_ctx = (c["L"] + n_steps + 63) // 64 * 64
         self.cfg = nosa.make_config(self.Bm, self.Hq, self.Hkv, c["k_q"], c["k_e"], self.max_ctx, c["offload"],
-                                    ck_bf16=c.get("ck_bf16", False), fill=c.get("fill", False))
+                                    ck_bf16=c.get("ck_bf16", False), fill=c.get("fill", False),
+                                    kv_format=c.get("kv_format", "bf16"))
         dev = torch.device(device)
         self.host = {}
         if c["offload"]:
@@ -132,7 +151,8 @@ class Workload:
         # append and select in one launch (it takes given logits and feeds the one-pass decode)
         self.fuse = bool(c.get("fuse", False)) and not (self.split or self.head)
         # the whole step of a layer in one launch (device store, union reading, given logits)
-        self.step = bool(c.get("step", False)) and not (self.split or self.head or c["offload"] or c.get("fill"))
+        self.step = bool(c.get("step", False)) and not (self.split or self.head or c["offload"] or c.get("fill") or
+                                                        kv8(c))
         self.W = [tuple(torch.from_numpy(w).to(dev) for w in synth.head_weights(seed, self.layer0 + l, self.Hkv))
                   for l in range(self.L)] if self.head else None
         self._prefill(dev)
@@ -365,9 +385,9 @@ def step_bytes(wl):
     c = wl.c
     nb = (c["L"] - 1) // 64
     if getattr(wl, "dense", False):
-        per_unit = (nb + 1) * (32768 + 256)
+        per_unit = attended_bytes(c, nb + 1)
     else:
-        per_unit = nb * 4 * 128 * ck_elem(c) + (c["k_q"] + c["k_e"] + 1) * (32768 + 256)
+        per_unit = nb * 4 * 128 * ck_elem(c) + attended_bytes(c, c["k_q"] + c["k_e"] + 1)
     return wl.L * wl.units * per_unit
 
 
@@ -378,17 +398,16 @@ def algo_bytes(c, U, Bm, Lctx, nsel_mean):
     unit.  Decode: the K, V and eviction logits of the attended blocks, the queries and the outputs.
     Append: the new K, V rows and logit.  The fused launches add up their parts."""
     nb_c = (Lctx - 1) // 64
-    blk = 64 * D * 2 * 2 + 64 * 4  # one block: keys + values (bf16) + eviction logits (fp32)
     a = {
         "select": U * (nb_c * 4 * D * ck_elem(c) + (c["Hq"] // c["Hkv"]) * D * 2),
-        "decode": U * nsel_mean * blk + 2 * Bm * c["Hq"] * D * 2,
+        "decode": U * attended_bytes(c, nsel_mean) + 2 * Bm * c["Hq"] * D * 2,
         "append": U * (2 * D * 2 + 4),
     }
     a["append_select"] = a["select"] + a["append"]
     a["step"] = a["append_select"] + a["decode"]
     n_res = min(c["k_e"], nb_c) + 1  # Gamma_e + the local block
-    a["resident"] = U * n_res * blk + Bm * c["Hq"] * D * 2
-    a["rest"] = U * max(nsel_mean - n_res, 0) * blk + 2 * Bm * c["Hq"] * D * 2
+    a["resident"] = U * attended_bytes(c, n_res) + Bm * c["Hq"] * D * 2
+    a["rest"] = (U * max(attended_bytes(c, nsel_mean) - attended_bytes(c, n_res), 0) + 2 * Bm * c["Hq"] * D * 2)
     return a
 
 
@@ -553,19 +572,20 @@ def load_peaks():
 # DRAM bytes per launch from an ncu capture (profiles/dram_traffic.json): used only for the
 # same workload variant and only while the kernel's sources are unchanged since the capture.
 KERNEL_SOURCES = {
-    "select": ("nosa_select.cu", "nosa_append_unit.cuh"), "decode": ("nosa_decode.cu", "nosa_attend.cuh"),
+    "select": ("nosa_select.cu", "nosa_append_unit.cuh"), "decode": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
     "step": ("nosa_step.cu", "nosa_attend.cuh", "nosa_append_unit.cuh"),
     "cache_sync": ("nosa_cache.cu",), "append": ("nosa_append.cu", "nosa_append_unit.cuh"),
     "append_select": ("nosa_select.cu", "nosa_append_unit.cuh"),
     # kernels that the benchmark's per-kernel pass does not time on its own (prefill, the split
     # decode's passes, the dense comparator, the cache plan): their captures are checked the same way
-    "dense": ("nosa_decode.cu", "nosa_attend.cuh"), "resident": ("nosa_decode.cu", "nosa_attend.cuh"),
-    "rest": ("nosa_decode.cu", "nosa_attend.cuh"),
+    "dense": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
+    "resident": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
+    "rest": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
     "cache_plan": ("nosa_cache.cu",), "cache_gather": ("nosa_cache.cu",),
     "append_head": ("nosa_append.cu", "nosa_append_unit.cuh"),
     "prefill_store": ("nosa_append.cu", "nosa_append_unit.cuh"),
     "prefill_pool": ("nosa_append.cu", "nosa_append_unit.cuh"),
-    "prefill_gamma": ("nosa_append.cu", "nosa_append_unit.cuh"),
+    "prefill_gamma": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_topk.cuh"),
     "prefill_head": ("nosa_append.cu", "nosa_append_unit.cuh"),
 }
 
@@ -615,7 +635,7 @@ def captured_traffic(name, c, args):
 def traffic_variant(c, args, name):
     """The workload variant a traffic capture of kernel `name` must match: the workload name plus the
     options that change that kernel's work (the layer count does not change a launch)."""
-    v = [args.workload]
+    v = [args.workload] + ([c["kv_format"]] if kv8(c) else [])
     for key in ("ck_bf16", "fill", "head", "split"):
         if c.get(key):
             v.append(key)
@@ -824,9 +844,9 @@ def run_nosa(args, c, rank, world, dev):
     if c["offload"] and fetched:
         fb = sum(fetched) / len(fetched) / (wl.L * wl.micro)  # blocks per launch (layer, micro-batch)
         avg = sum(kt["cache_sync"]) / len(kt["cache_sync"])
-        gbs = fb * 32768 / (avg * 1e-3) / 1e9
-        kern["cache_sync"].update({"bytes": fb * 32768, "GBps": gbs, "frac_pcie": gbs / pcie})
-        step_gbs = sum(fetched) / len(fetched) * 32768 / (ms / args.steps * 1e-3) / 1e9
+        gbs = fb * block_bytes(c) / (avg * 1e-3) / 1e9
+        kern["cache_sync"].update({"bytes": fb * block_bytes(c), "GBps": gbs, "frac_pcie": gbs / pcie})
+        step_gbs = sum(fetched) / len(fetched) * block_bytes(c) / (ms / args.steps * 1e-3) / 1e9
         pcie_obj = {"fetched_blocks_per_step": sum(fetched) / len(fetched),
                     "fetched_blocks_per_unit_step": fb / U, "achieved_GBps": gbs, "peak_GBps": pcie,
                     "peak": "measured pinned cudaMemcpyAsync H2D, 1 GiB, this box", "frac": gbs / pcie,
@@ -948,6 +968,7 @@ def run_nosa(args, c, rank, world, dev):
         "config": {"workload": f"{args.workload}: " + describe(c, args.host_groups), "layers": c["layers"],
                    "batch": c["B"], "heads_q": c["Hq"], "heads_kv": c["Hkv"], "context": c["L"], "k_q": c["k_q"],
                    "k_e": c["k_e"], "offload": c["offload"], "pooled_keys": "bf16" if c.get("ck_bf16") else "fp32",
+                   "kv_format": c.get("kv_format", "bf16"),
                    "selection": "fill" if c.get("fill") else "union",
                    "eviction_logits": "fused head" if c.get("head") else "input",
                    "decode": "split (resident during select / cache sync, then rest)" if c.get("split") else "one pass", "host_kv_groups": args.host_groups if c["offload"] else None,
@@ -980,7 +1001,7 @@ def run_dense(args, c, rank, world, dev):
     small = step_bytes(wl) < 2 * L2_BYTES
     per = time_idempotent(wl, "dense", reps=3, flush=L2Flusher(dev) if small else None)
     Lctx = c["L"] + n
-    nbytes = wl.units * ((Lctx + 63) // 64) * (64 * D * 2 * 2 + 64 * 4) + 2 * wl.B * c["Hq"] * D * 2
+    nbytes = wl.units * attended_bytes(c, (Lctx + 63) // 64) + 2 * wl.B * c["Hq"] * D * 2
     hbm_peak, peak_kind = load_peaks()
     gbs = nbytes / (per * 1e-3) / 1e9
     errs = [lay.read_error() for per_layer in wl.layers for lay in per_layer]
@@ -1115,8 +1136,13 @@ def main():
                     help="split decode: attend Gamma_e + the local block while select and the cache sync run")
     ap.add_argument("--fill", action="store_true",
                     help="fill reading of the selection: Gamma_e fills the remainder outside Gamma_q")
+    ap.add_argument("--kv-format", default="bf16", choices=["bf16", "int8", "e4m3"],
+                    help="how the KV store holds its blocks (8 bits: a scale per block; a layer's step is then "
+                         "append + select and the decode)")
     args = ap.parse_args()
     c = dict(WORKLOADS[args.workload])
+    if args.kv_format != "bf16":
+        c["kv_format"] = args.kv_format
     if args.ck_bf16:
         c["ck_bf16"] = True
     if args.fill:

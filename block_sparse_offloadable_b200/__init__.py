@@ -413,6 +413,8 @@ class NosaLayer:
         kept = torch.empty((self.units, max(int(keep), 0) + 1), dtype=torch.int32, device=self.device)
         nosa_evict(self.cfg, self.state, self.weights, keep, sink, recent, dst.cfg, dst.state, dst.weights, kept,
                    stream)
+        if stream is not None:
+            kept.record_stream(stream)
         return kept
 
     def kv8_views(self):

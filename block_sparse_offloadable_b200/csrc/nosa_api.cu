@@ -12,6 +12,7 @@ using namespace nosa;
 namespace {
 
 constexpr int64_t kMaxCtx = 1ll << 20;
+constexpr size_t kL2Bytes = 126u << 20;
 constexpr int32_t kKv8Flags = NOSA_FLAG_KV_INT8 | NOSA_FLAG_KV_E4M3;
 
 struct Geo {
@@ -454,6 +455,11 @@ int make_select(const nosa_config *c, const nosa_state *st, const uint16_t *q, i
     p.chunk_blocks = c->k_q > 0 ? select_chunk_blocks(p.units, p.nblk, (c->flags & NOSA_FLAG_CK_BF16) != 0) : p.nblk;
     p.k_q = c->k_q; p.k_e = c->k_e; p.max_sel = (int32_t)g.max_sel; p.scale = c->scale;
     p.ck_bf16 = (c->flags & NOSA_FLAG_CK_BF16) != 0;
+    p.k8 = fmt_of(c) != kFmtBf16;
+    // A large launch's pooled keys would push out of L2 what the attention over codes needs again, its
+    // instructions above all: append + select and decode of a layer, 32 x 32K (68 MB of keys), int8:
+    // 45.7 us, 42.2 where the keys go first; 4 x 32K (9 MB), all in L2: 24.3 and 25.4.
+    p.once = p.k8 && nosa_state_bytes(c, NOSA_BUF_CK) > kL2Bytes / 4;
     p.fill = (c->flags & NOSA_FLAG_FILL) != 0;
     p.pool = p.fill ? st->pool : nullptr; p.pool_n = p.fill ? st->pool_n : nullptr;
     p.gamma_e_out = p.fill ? st->gamma_e : nullptr; p.gamma_n_out = p.fill ? st->gamma_n : nullptr;

@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
         }
         return i;
     };
+    const uint64_t once = evict_first_policy();
     // Item number `it` of the CTA, by one thread; nt: the tails before it.
     const auto issue = [&](const Item &i, int it, int nt) {
         const int s = it % kStages;
@@ -350,11 +351,11 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             if (ok) {
                 const int32_t y = (int32_t)(((int64_t)i.u * p.blocks_per_unit + i.pb) * 2 * kBlock);
                 mbar_arrive_expect_tx(&full[s], kBlockBytes + kBlock * sizeof(float));
-                tma_load_2d(t, &tmap, &full[s], 0, y);
-                tma_load_2d(t + kBoxBytes, &tmap, &full[s], 64, y);
-                tma_load_2d(t + 2 * kBoxBytes, &tmap, &full[s], 0, y + kBlock);
-                tma_load_2d(t + 3 * kBoxBytes, &tmap, &full[s], 64, y + kBlock);
-                bulk_load(es, p.e + (int64_t)i.u * p.max_ctx + (int64_t)i.lb * kBlock, kBlock * sizeof(float), &full[s]);
+                tma_load_2d_hint(t, &tmap, &full[s], 0, y, once);
+                tma_load_2d_hint(t + kBoxBytes, &tmap, &full[s], 64, y, once);
+                tma_load_2d_hint(t + 2 * kBoxBytes, &tmap, &full[s], 0, y + kBlock, once);
+                tma_load_2d_hint(t + 3 * kBoxBytes, &tmap, &full[s], 64, y + kBlock, once);
+                bulk_load_hint(es, p.e + (int64_t)i.u * p.max_ctx + (int64_t)i.lb * kBlock, kBlock * sizeof(float), &full[s], once);
             } else {
                 mbar_arrive(&full[s]);
             }
@@ -373,11 +374,11 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 const int32_t y = i.u * 2 * kBlock;
                 uint8_t *tv = tails + tb * kHalfBlockBytes;
                 mbar_arrive_expect_tx(&full[s], kBlockBytes + kBlock * sizeof(float));
-                tma_load_2d(t, &tail_map, &full[s], 0, y);
-                tma_load_2d(t + kBoxBytes, &tail_map, &full[s], 64, y);
-                tma_load_2d(tv, &tail_map, &full[s], 0, y + kBlock);
-                tma_load_2d(tv + kBoxBytes, &tail_map, &full[s], 64, y + kBlock);
-                bulk_load(es, p.e + (int64_t)i.u * p.max_ctx + (int64_t)i.lb * kBlock, kBlock * sizeof(float), &full[s]);
+                tma_load_2d_hint(t, &tail_map, &full[s], 0, y, once);
+                tma_load_2d_hint(t + kBoxBytes, &tail_map, &full[s], 64, y, once);
+                tma_load_2d_hint(tv, &tail_map, &full[s], 0, y + kBlock, once);
+                tma_load_2d_hint(tv + kBoxBytes, &tail_map, &full[s], 64, y + kBlock, once);
+                bulk_load_hint(es, p.e + (int64_t)i.u * p.max_ctx + (int64_t)i.lb * kBlock, kBlock * sizeof(float), &full[s], once);
             } else {
                 mbar_arrive(&full[s]);
             }
@@ -390,8 +391,8 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             if (ok) {
                 const int64_t rb = (int64_t)i.u * p.blocks_per_unit + i.pb;
                 mbar_arrive_expect_tx(&full[s], kHeld8Bytes);
-                tma_load_3d(t, &tmap, &full[s], 0, 0, (int32_t)rb);
-                bulk_load(es, p.records + rb * kRec8Bytes + kBlock8Bytes, kSide8Bytes, &full[s]);
+                tma_load_3d_hint(t, &tmap, &full[s], 0, 0, (int32_t)rb, once);
+                bulk_load_hint(es, p.records + rb * kRec8Bytes + kBlock8Bytes, kSide8Bytes, &full[s], once);
             } else {
                 mbar_arrive(&full[s]);
             }

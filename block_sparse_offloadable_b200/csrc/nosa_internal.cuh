@@ -59,6 +59,8 @@ struct SelectParams {
     int32_t *pool_n;          // [u]
     int32_t nsub, nblk, G, units, nchunks, chunk_blocks, k_q, k_e, max_sel, ck_bf16, fill;
     float scale;
+    int32_t k8;               // over an 8-bit KV store
+    int32_t once;             // with k8: the pooled keys are evicted from L2 first
     int32_t fused;            // append this step's token first (chunk 0's extra warp), see nosa_select.cu
     AppendParams ap;          // the append's parameters when fused (T = 1)
 };

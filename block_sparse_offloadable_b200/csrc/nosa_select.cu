@@ -140,7 +140,8 @@ int select_chunk_blocks(int32_t units, int32_t nblk, bool ck_bf16) {
     return (int)per;
 }
 
-template <typename T>
+// k8: over an 8-bit KV store (the append codes blocks; see SelectParams::once).
+template <typename T, bool k8>
 __global__ void __launch_bounds__((kSelW + 2) * 32) select_kernel(const SelectParams p) {
     constexpr int kSelS = SelGeo<T>::kStages;
     constexpr int kStageBytes = stage_bytes<T>();
@@ -201,7 +202,11 @@ __global__ void __launch_bounds__((kSelW + 2) * 32) select_kernel(const SelectPa
                 const int s = i % kSelS;
                 const uint32_t bytes = (uint32_t)min(kSelSB, bend - bs) * (kSubPerBlock * kD * SelGeo<T>::kElem);
                 mbar_arrive_expect_tx(&full[s], bytes);
-                bulk_load(tiles + s * kStageBytes, ck + (int64_t)bs * kSubPerBlock * kD, bytes, &full[s]);
+                if (k8 && p.once)
+                    bulk_load_hint(tiles + s * kStageBytes, ck + (int64_t)bs * kSubPerBlock * kD, bytes, &full[s],
+                                   evict_first_policy());
+                else
+                    bulk_load(tiles + s * kStageBytes, ck + (int64_t)bs * kSubPerBlock * kD, bytes, &full[s]);
             };
             // The first ring of stages goes out before this thread has the context length: the
             // chunk is bounded by the largest candidate count max_ctx allows, and the stages of
@@ -231,10 +236,7 @@ __global__ void __launch_bounds__((kSelW + 2) * 32) select_kernel(const SelectPa
         }
     } else if (warp == kSelW + 1) {
         // the fused append (launched only when fused): chunk 0 of each unit
-        if (chunk == 0) {  // fences before its hand-off
-            if (p.ap.fmt == kFmtBf16) append_unit<false>(p.ap, u, lane, p.ap.e_new[u], false);
-            else append_unit<true>(p.ap, u, lane, p.ap.e_new[u], false);
-        }
+        if (chunk == 0) append_unit<k8>(p.ap, u, lane, p.ap.e_new[u], false);  // fences before its hand-off
     } else {
         // q_hat = sum of the G query heads of this kv head, lane's 4 dims; the
         // loads are issued together while the first stages are in flight
@@ -399,21 +401,23 @@ __global__ void __launch_bounds__((kSelW + 2) * 32) select_kernel(const SelectPa
     for (int i = total + 1 + lane; i < p.max_sel; i += 32) sel[i] = -1;
 }
 
-template <typename T>
+template <typename T, bool k8>
 int launch_select_t(const SelectParams &p, cudaStream_t stream) {
     const size_t smem = select_smem_bytes<T>(p.nblk);
-    if (cudaFuncSetAttribute(select_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(select_kernel<T, k8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem) != cudaSuccess)
         return NOSA_ERR_CUDA;
     dim3 grid(p.nchunks, p.units);
-    return launch_pdl(select_kernel<T>, grid, dim3((kSelW + 1 + (p.fused ? 1 : 0)) * 32), smem, stream, p) ==
+    return launch_pdl(select_kernel<T, k8>, grid, dim3((kSelW + 1 + (p.fused ? 1 : 0)) * 32), smem, stream, p) ==
                    cudaSuccess
                ? NOSA_OK
                : NOSA_ERR_CUDA;
 }
 
 int launch_select(const SelectParams &p, cudaStream_t stream) {
-    return p.ck_bf16 ? launch_select_t<__nv_bfloat16>(p, stream) : launch_select_t<float>(p, stream);
+    if (p.k8)
+        return p.ck_bf16 ? launch_select_t<__nv_bfloat16, true>(p, stream) : launch_select_t<float, true>(p, stream);
+    return p.ck_bf16 ? launch_select_t<__nv_bfloat16, false>(p, stream) : launch_select_t<float, false>(p, stream);
 }
 
 }  // namespace nosa

@@ -276,6 +276,55 @@ def test_eviction_head_and_ragged_offload(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("offload", [False, True])
+def test_fill_reading_and_bf16_pooled_keys(fmt, offload):
+    L, steps = 64 * 14 + 40, 60
+    t = H.Tokens(2, 8, 2, L + steps, seed=18)
+    lay, ref = (H.layer(t, 64 * 18, f, k_q=3, k_e=4, offload=offload, fill=True, ck_bf16=True) for f in (fmt, "bf16"))
+    out, rout = (torch.empty((2, 8, 128), dtype=torch.int16, device="cuda") for _ in range(2))
+    for x in (lay, ref):
+        t.prefill(x, L)
+    for i in range(steps):
+        q = t.q()
+        for x, o in ((lay, out), (ref, rout)):
+            x.decode_step(*t.new(np.full(t.units, L + i)), H.dev16(q), o)
+        assert torch.equal(lay.sel, ref.sel) and torch.equal(lay.pool_n, ref.pool_n) and torch.equal(lay.gq, ref.gq)
+        assert not offload or torch.equal(lay.n_fetched, ref.n_fetched)
+        if i % 13 == 0:
+            H.check_out(t, out, q, [t.unit(u, L + i + 1, fmt) for u in range(t.units)], H.sels(lay))
+    assert lay.read_error() == 0
+
+
+@pytest.mark.parametrize("fmt,offload", [("int8", True), ("e4m3", False)])
+def test_full_size_layer(fmt, offload):
+    # one layer of the 128K offload workload (and of the 32K device one), as bench.py runs it: the
+    # selection and the fetches of the bf16 store, the attention of the plain form
+    import bench
+    c = dict(bench.WORKLOADS["offload28-128k" if offload else "stack28-32k"], step=False)
+    seen = {}
+    for f in ("bf16", fmt):  # one after the other: workloads share their pinned host store
+        wl = bench.Workload(dict(c, kv_format=f), 3, seed=4, layers=1)
+        lay, seen[f] = wl.layers[0][0], []
+        for i in range(3):
+            wl.cur.copy_(wl.inputs[i])
+            q, k, v, e = wl.views(wl.cur, 0)
+            out = torch.empty_like(q)
+            lay.decode_step(k, v, e, q, out)
+            seen[f] += [lay.sel.clone()] + ([lay.n_fetched.clone()] if offload else [])
+        assert lay.read_error() == 0
+    assert all(torch.equal(x, y) for x, y in zip(seen["bf16"], seen[fmt]))
+    import synth
+    n = c["L"] + 3
+    sel, got = lay.sel.cpu().numpy(), H.out_of(out).reshape(lay.units, -1, 128)
+    qq = P.bf16(q.cpu().numpy()).reshape(lay.units, -1, 128)
+    for u in (0, lay.units - 1):
+        K, V = (P.bf16(synth.kv_rows(4, s, 0, u // 2, u % 2, 0, n)) for s in (synth.K_STREAM, synth.V_STREAM))
+        ref = P.Unit(K, V, synth.e_rows(4, 0, u // 2, u % 2, 0, n).astype(np.float64), fmt, lay.G, 128 ** -0.5)
+        want, tol = ref.attend(qq[u], [x for x in sel[u] if x >= 0])[:2]
+        assert (np.abs(got[u] - want) <= tol).all(), u
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_offsets_past_32_bits(fmt):
     # 32 units of 2^20 tokens: 8.6 GB of codes; the last unit's blocks lie past 2^32 bytes
     t = H.Tokens(16, 4, 2, 200, seed=15)
