@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kItemCons = 5;                       // consumer warps
 constexpr int kItemProd = 2;                       // producer warps
+constexpr int kAlignItems = 6;                     // about what a segment's end costs, in items
 constexpr int kItemConsThreads = kItemCons * 32;
 constexpr int kItemThreads = (kItemCons + kItemProd) * 32;
 
@@ -312,17 +313,44 @@ __global__ void __launch_bounds__(kItemThreads, 1)
     // Balanced: ranges over Ge CTAs of no fewer items than consumer warps, where there are as many: a
     // CTA with one item costs a merge of its state and saves nothing (65 blocks a unit, 2 units: 12.0 us
     // with ranges of 5, 14.4 of 8 over 4 warps, 15.6 of 4).
-    const int32_t C = p.pieces;
     const int32_t We = (W + kTakers - 1) / kTakers;
     const int32_t Ge = min(max(We, 1), grid);
-    int32_t lo, hi;
-    if (C > 0) {
-        const int32_t rc = cta % C;
-        lo = cta / C * p.max_sel + rc * p.max_sel / C;
-        hi = cta / C * p.max_sel + (rc + 1) * p.max_sel / C;
+    // Where a CTA has items of one unit alone, that unit's CTAs: `team` of them from team_first on.
+    int32_t lo, hi, team = p.pieces, team_first = 0;
+    if (team > 0) {  // equal pieces of every unit
+        team_first = cta / team * team;
+        lo = cta / team * p.max_sel + (cta - team_first) * p.max_sel / team;
+        hi = cta / team * p.max_sel + (cta - team_first + 1) * p.max_sel / team;
     } else {
         lo = (int32_t)((cta < Ge) ? (int64_t)cta * W / Ge : W);
         hi = (int32_t)((cta < Ge) ? (int64_t)(cta + 1) * W / Ge : W);
+    }
+    if (p.pieces <= 0 && U <= 32 && U <= Ge && W > 0) {
+        // Few units, of any lengths: a CTA for each and the others in proportion to the units' items, equal
+        // pieces of a unit each, if that gives no CTA more than kAlignItems items more than balanced
+        // ranges.  It spares ranges with two units in them, whose first one's end holds up the stream (16
+        // units of 129 to 257 blocks, with weights: 24.2 us, balanced 27.7).
+        const int32_t n = lane < U ? first_item(lane + 1) - first_item(lane) : 0;
+        const int32_t mine = n > 0 ? 1 + (int32_t)((int64_t)n * (Ge - U) / W) : 0;  // Ge in all at most
+        const int32_t most = (int32_t)__reduce_max_sync(0xFFFFFFFFu, n > 0 ? (uint32_t)((n + mine - 1) / mine) : 0u);
+        int32_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const int uc = __popc(__ballot_sync(0xFFFFFFFFu, incl <= cta));  // 32: no unit's
+        const int32_t t = __shfl_sync(0xFFFFFFFFu, mine, uc & 31), tf = __shfl_sync(0xFFFFFFFFu, incl - mine, uc & 31);
+        if (most <= (W + Ge - 1) / Ge + kAlignItems) {
+            team = t;
+            team_first = tf;
+            lo = hi = W;
+            if (uc < U) {
+                const int32_t at = first_item(uc), nu = first_item(uc + 1) - at;
+                lo = at + (cta - team_first) * nu / team;
+                hi = at + (cta - team_first + 1) * nu / team;
+            }
+        }
     }
     const int32_t n_items = hi - lo;
 
@@ -523,7 +551,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 // hand-off: the partial is written (barrier), one thread counts it with release
                 // semantics; the unit's last contributor acquired the others' partials with the same
                 // atomic, and the barrier after it orders every thread's later loads after them
-                const int32_t others = C > 0 ? C - 1 : cta_of((int64_t)u_end - 1, W, Ge) - cta_of(u_begin, W, Ge);
+                const int32_t others = team > 0 ? team - 1 : cta_of((int64_t)u_end - 1, W, Ge) - cta_of(u_begin, W, Ge);
                 if (ctid == 0) s_last = (int32_t)atom_add_acq_rel_gpu(p.counter + u, 1u) == others;
                 consumer_sync<kItemConsThreads>();
                 if (s_last) (slot == 0 ? last_first : last_other) = u;
@@ -543,8 +571,8 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             const int32_t um = k ? last_other : last_first;
             if (um < 0) continue;
             const int32_t u_begin = first_item(um), u_end = first_item(um + 1);
-            const int32_t cf = C > 0 ? um * C : cta_of(u_begin, W, Ge);
-            const int32_t cl = C > 0 ? um * C + C - 1 : cta_of((int64_t)u_end - 1, W, Ge);
+            const int32_t cf = team > 0 ? team_first : cta_of(u_begin, W, Ge);
+            const int32_t cl = team > 0 ? team_first + team - 1 : cta_of((int64_t)u_end - 1, W, Ge);
             if (ctid == 0) p.counter[um] = 0;
             // the CTA partials in CTA order (and, merging the rest pass, the resident state)
             const int nc = cl - cf + 1 + (p.mode == kModeRest ? 1 : 0);  // <= Ge + 1
@@ -554,7 +582,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 if (cc > cl) {
                     src[t] = p.res_part + (int64_t)um * kPartFloats;
                 } else {
-                    const int sl = (C > 0 || unit_of((int32_t)((int64_t)cc * W / Ge)) == um) ? 0 : 1;
+                    const int sl = (team > 0 || unit_of((int32_t)((int64_t)cc * W / Ge)) == um) ? 0 : 1;
                     src[t] = p.part + (int64_t)(cc * 2 + sl) * kPartFloats;
                 }
             }

@@ -27,7 +27,9 @@ def check_weights(t, got, before, q, units, blocks, nblk):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("B,Hq,Hkv,lens", [(1, 1, 1, [1]), (1, 8, 1, [65]), (3, 7, 1, [0, 1000, 63]),
                                            (1, 10, 2, [64 * 70 + 1]), (24, 8, 2, [64 * 60 - 100 * i for i in range(24)]), (1, 16, 2, [64 * 300]),
-                                           (40, 16, 4, [65 + 7 * i for i in range(40)])])
+                                           (40, 16, 4, [65 + 7 * i for i in range(40)]),
+                                           (24, 4, 1, [64 * 700] + [1 + i for i in range(23)]),  # one long, many short
+                                           (6, 8, 2, [0, 64 * 90, 64, 0, 1, 64 * 33 + 1])])
 def test_dense_weights(fmt, B, Hq, Hkv, lens):
     T = max(lens)
     t = H.Tokens(B, Hq, Hkv, T, seed=B + T)
