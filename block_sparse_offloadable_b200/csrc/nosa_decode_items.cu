@@ -11,8 +11,9 @@
 // instructions than a bf16 one:
 //  * One consumer warp attends a whole block (nosa_attend8.cuh).  Five of them (three over the bf16
 //    store) with two stages each: a stage's next block is in flight while its other one is
-//    attended.  Eight warps with ten stages leave two blocks in flight while all attend: 93 us
-//    where this takes 75 at 32 ragged sequences of up to 32K (e4m3, 16 q / 2 kv heads).
+//    attended.  Eight warps with ten stages leave two blocks in flight while all attend: 93 us at
+//    32 ragged sequences of up to 32K (e4m3, 16 q / 2 kv heads) where five warps took 75 (70 now,
+//    0.89 of the measured HBM rate).
 //  * Two producer warps, for the even and the odd items: one issue (expected bytes, a tensor copy of
 //    the codes, a bulk copy of the logits and scales) takes 0.27 us of one thread's time, and a
 //    block must come every 0.38 us to keep the memory busy; the first items are issued by the
@@ -126,12 +127,13 @@ __device__ __forceinline__ void merge_resident4(const DecodeParams &p, int32_t u
     merge_resident(p, u, h, d4 + 3, M, acc.w, lsum);
 }
 
-// The last CTA of a unit merges the nc partial records src[], in order.  A thread takes 8 dims of a head and has the loads of kBatch records in flight at
-// once, since a round trip to the L2 (0.7 us) is what this costs.  Writes bf16 out, or the merged
-// record to res (the split decode's state); s_lse: the log2 of each head's whole sum.
+// The last CTA of a unit merges the nc partial records src[], in order.  A thread takes 8 dims of a
+// head and has the loads of kBatch records in flight at once, since a round trip to the L2 (0.7 us) is
+// what this costs.  Writes bf16 out, or the merged record to res (the split decode's state); s_lse: the
+// log2 of each head's whole sum.
 template <bool kNan>
-__device__ __forceinline__ void merge_records(const float *const *src, int nc, int G, uint16_t *out,
-                                           float *res, float *s_lse, int ctid) {
+__device__ __forceinline__ void merge_records(const float *const *src, int nc, int G, uint16_t *out, float *res,
+                                              float *s_lse, int ctid) {
     constexpr int kBatch = 4;
 #pragma unroll 1
     for (int v = ctid; v < G * (kD / 8); v += kItemConsThreads) {

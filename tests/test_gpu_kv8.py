@@ -92,7 +92,8 @@ def test_decode_from_empty_over_block_borders(fmt, offload, how):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("B,Hq,Hkv,lens", [
     (1, 1, 1, [1]), (1, 8, 1, [64]), (1, 3, 1, [65]), (2, 10, 2, [128, 129]), (3, 7, 1, [0, 1000, 63]),
-    (1, 16, 2, [64 * 70 + 1]), (24, 8, 2, [64 * 60 - 100 * i for i in range(24)]), (5, 16, 16, [200, 64, 65, 0, 511]), (40, 16, 4, [65 + 7 * i for i in range(40)])])
+    (1, 16, 2, [64 * 70 + 1]), (24, 8, 2, [64 * 60 - 100 * i for i in range(24)]), (5, 16, 16, [200, 64, 65, 0, 511]), (40, 16, 4, [65 + 7 * i for i in range(40)]),
+    (2048, 2, 1, [1 + i % 130 for i in range(2048)])])  # as many units as a call takes
 def test_dense(fmt, B, Hq, Hkv, lens):
     T = max(lens)
     t = H.Tokens(B, Hq, Hkv, T, seed=B + T)

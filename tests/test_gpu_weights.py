@@ -29,7 +29,8 @@ def check_weights(t, got, before, q, units, blocks, nblk):
                                            (1, 10, 2, [64 * 70 + 1]), (24, 8, 2, [64 * 60 - 100 * i for i in range(24)]), (1, 16, 2, [64 * 300]),
                                            (40, 16, 4, [65 + 7 * i for i in range(40)]),
                                            (24, 4, 1, [64 * 700] + [1 + i for i in range(23)]),  # one long, many short
-                                           (6, 8, 2, [0, 64 * 90, 64, 0, 1, 64 * 33 + 1])])
+                                           (6, 8, 2, [0, 64 * 90, 64, 0, 1, 64 * 33 + 1]),
+                                           (2048, 2, 1, [1 + i % 130 for i in range(2048)])])  # the most units
 def test_dense_weights(fmt, B, Hq, Hkv, lens):
     T = max(lens)
     t = H.Tokens(B, Hq, Hkv, T, seed=B + T)
@@ -310,3 +311,22 @@ def test_evict_captured_and_refused():
     with pytest.raises(nosa.NosaError) as ei:
         nosa.nosa_evict(src.cfg, src.state, src.weights.cpu(), 5, 0, 0, dst.cfg, dst.state, dst.weights, kept)
     assert ei.value.code == nosa.ERR_PTR
+
+
+def test_evict_on_another_stream():
+    # the list of kept blocks is the given stream's memory: nothing queued on the current one holds it
+    t = H.Tokens(2, 4, 2, 64 * 12, seed=36)
+    src, dst = (H.layer(t, n, "int8", k_q=2, k_e=2, weights=True) for n in (64 * 13, 64 * 6))
+    t.prefill(src, 64 * 12)
+    src.weights.uniform_(generator=torch.Generator("cuda").manual_seed(3))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        busy = torch.full((4, 6), 77, dtype=torch.int32, device="cuda")  # freed while it may still be written
+        del busy
+        kept = src.evict(dst, 5, stream=s)
+        s.synchronize()
+        with torch.cuda.stream(s):
+            got = kept.cpu()
+        for u in range(4):
+            assert got[u].tolist() == P.keep_blocks(src.weights[u].cpu().numpy(), 11, 5, 0, 0) + [11]
