@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(256) prefill_pool_kernel(const AppendParams p)
 }
 
 // A block's rows (bf16, in the registers of a CTA of 256 threads: thread's piece i is piece
-// tid + 256 i of the keys and of the values; e: its logits) to the record dst.  Two barriers.
+// tid + 256 i of the keys and of the values; e: its logits) to the record dst.  ks: the keys in shared
+// memory, from which they are coded so that their registers end with the maximum; or null.  Two barriers.
 __device__ __forceinline__ void code_block(const uint4 (&k)[4], const uint4 (&v)[4], const float *e, uint8_t *dst,
-                                           uint32_t (*s_max)[8], int fmt) {
+                                           uint32_t (*s_max)[8], int fmt, const uint4 *ks = nullptr) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t ak = 0, av = 0;
 #pragma unroll
@@ -188,7 +189,7 @@ __device__ __forceinline__ void code_block(const uint4 (&k)[4], const uint4 (&v)
     uint2 *to = reinterpret_cast<uint2 *>(dst) + tid;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        to[256 * i] = code8(k[i], sk.y, fmt);
+        to[256 * i] = code8(ks ? ks[tid + 256 * i] : k[i], sk.y, fmt);
         to[kHalfBlock8Bytes / 8 + 256 * i] = code8(v[i], sv.y, fmt);
     }
     float *side = reinterpret_cast<float *>(dst + kBlock8Bytes);
@@ -200,8 +201,11 @@ __device__ __forceinline__ void code_block(const uint4 (&k)[4], const uint4 (&v)
 // rows in registers (8 pieces of 16 bytes a thread), finds both largest magnitudes, and writes the
 // codes; the keys also go to shared memory, where the pooled means are summed (thread = sub-block
 // and pair of dims, in row order).  The newest block's rows go to the tail as they are.  Reads
-// 33 KiB and writes 19 KiB a block; bound by HBM.
-__global__ void __launch_bounds__(256) prefill_store8_kernel(const AppendParams p) {
+// 33 KiB and writes 19 KiB a block; bound by HBM.  The keys are coded from shared memory: 40 registers,
+// six CTAs an SM.  32 sequences of up to 32K (2 kv heads, bf16 pooled keys), the whole call: 204 us, 0.93
+// of the measured HBM rate; coded from registers 221 (four CTAs), 216 to 220 (five), 227 to 231 (six,
+// spills); with streaming stores 230.
+__global__ void __launch_bounds__(256, 6) prefill_store8_kernel(const AppendParams p) {
     __shared__ __align__(16) uint8_t ks[kHalfBlockBytes];
     __shared__ uint32_t s_max[2][8];
     __shared__ float s_e[kBlock];
@@ -242,7 +246,8 @@ __global__ void __launch_bounds__(256) prefill_store8_kernel(const AppendParams 
                 tail[kHalfBlockBytes / 16 + tid + 256 * i] = v[i];
             }
     } else {
-        code_block(k, v, s_e, p.store + ((int64_t)u * p.nblk + blk) * kRec8Bytes, s_max, p.fmt);
+        code_block(k, v, s_e, p.store + ((int64_t)u * p.nblk + blk) * kRec8Bytes, s_max, p.fmt,
+                   reinterpret_cast<const uint4 *>(ks));
     }
     // pooled keys: thread = (sub-block, pair of dims)
     const int sub = tid >> 6, pair = tid & 63;
