@@ -410,8 +410,12 @@ class NosaLayer:
         the sequences.  Returns the kept blocks' numbers, int32 [units][keep + 1], -1 padded."""
         self._need_weights()
         dst._need_weights()
-        with torch.cuda.stream(stream):  # kept is of that stream's memory
-            kept = torch.empty((self.units, max(int(keep), 0) + 1), dtype=torch.int32, device=self.device)
+        shape = (self.units, max(int(keep), 0) + 1)
+        if stream is None:
+            kept = torch.empty(shape, dtype=torch.int32, device=self.device)
+        else:
+            with torch.cuda.stream(stream):  # kept is of that stream's memory
+                kept = torch.empty(shape, dtype=torch.int32, device=self.device)
         nosa_evict(self.cfg, self.state, self.weights, keep, sink, recent, dst.cfg, dst.state, dst.weights, kept,
                    stream)
         return kept
