@@ -572,21 +572,25 @@ def load_peaks():
 # DRAM bytes per launch from an ncu capture (profiles/dram_traffic.json): used only for the
 # same workload variant and only while the kernel's sources are unchanged since the capture.
 KERNEL_SOURCES = {
-    "select": ("nosa_select.cu", "nosa_append_unit.cuh"), "decode": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
-    "step": ("nosa_step.cu", "nosa_attend.cuh", "nosa_append_unit.cuh"),
-    "cache_sync": ("nosa_cache.cu",), "append": ("nosa_append.cu", "nosa_append_unit.cuh"),
-    "append_select": ("nosa_select.cu", "nosa_append_unit.cuh"),
+    "select": ("nosa_select.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"), "decode": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
+    "step": ("nosa_step.cu", "nosa_attend.cuh", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
+    "cache_sync": ("nosa_cache.cu",), "append": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
+    "append_select": ("nosa_select.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
     # kernels that the benchmark's per-kernel pass does not time on its own (prefill, the split
     # decode's passes, the dense comparator, the cache plan): their captures are checked the same way
     "dense": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
     "resident": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
     "rest": ("nosa_decode.cu", "nosa_decode_work.cuh", "nosa_attend.cuh"),
     "cache_plan": ("nosa_cache.cu",), "cache_gather": ("nosa_cache.cu",),
-    "append_head": ("nosa_append.cu", "nosa_append_unit.cuh"),
-    "prefill_store": ("nosa_append.cu", "nosa_append_unit.cuh"),
-    "prefill_pool": ("nosa_append.cu", "nosa_append_unit.cuh"),
-    "prefill_gamma": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_topk.cuh"),
-    "prefill_head": ("nosa_append.cu", "nosa_append_unit.cuh"),
+    "append_head": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
+    "prefill_store": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
+    "prefill_pool": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
+    "prefill_gamma": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh", "nosa_topk.cuh"),
+    "prefill_head": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
+    # the 8-bit store's own kernels ("decode" over it is "decode8")
+    "decode8": ("nosa_decode_items.cu", "nosa_decode_work.cuh", "nosa_attend8.cuh", "nosa_attend.cuh"),
+    "dense8": ("nosa_decode_items.cu", "nosa_decode_work.cuh", "nosa_attend8.cuh", "nosa_attend.cuh"),
+    "prefill_store8": ("nosa_append.cu", "nosa_append_unit.cuh", "nosa_kv8.cuh"),
 }
 
 
@@ -624,6 +628,8 @@ def captured_traffic(name, c, args):
     except (OSError, ValueError):
         return None, "no capture"
     variant = traffic_variant(c, args, name)
+    if kv8(c) and name + "8" in KERNEL_SOURCES:
+        name += "8"
     for e in table.get("captures", []):
         if e.get("kernel") == name and e.get("variant") == variant:
             if e.get("sources_sha256") != sources_sha(name):
