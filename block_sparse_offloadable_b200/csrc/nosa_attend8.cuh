@@ -56,15 +56,46 @@ struct Dims8 {  // one 16-byte chunk of a 128-byte row
     static __device__ __forceinline__ int at(int x) { return x ^ ((x >> 5) & 1) ^ (((x >> 6) & 1) << 3); }
 };
 
-// Leave an item's weights, per head, for the unit's last CTA: the log2 of the sum of 2^x over its
-// tokens (s0, s1: this lane's sums relative to m0, m1; -inf where nothing is seen).  rec: 8 values.
-__device__ __forceinline__ void leave_weights(float *rec, float s0, float s1, float m0, float m1, int r, int c) {
+// An item's sums of 2^x, for heads 2c and 2c + 1 and this lane's tokens: s0 and s1, relative to m0 and m1.
+struct ItemSums {
+    float s0, s1, m0, m1;
+};
+
+// Leave an item's weights, per head, for the unit's last CTA: rec[h] = v, the log2 of the sum of 2^x over
+// its tokens, -inf where nothing is seen.  A weight wants v to an absolute error, and next to a large m a
+// float holds none of log2(s): a unit whose logits all lie at -1e9, or at the lowest finite value, would have no
+// shares left.  What the heads' x have in common is the logit.  So there v is taken against the item's
+// largest logit, which is found again in the store when it is wanted (e, n: the item's logits in
+// shared memory), and left as 2^40 v, at least 2^16 in magnitude; a plain v stays below 2^12.  Up to kNear a
+// plain v, below 256, is off by no more than an x of that size (half a step: 2^-17).  *far: set if some v is not
+// plain; adding the weights up then reads the logits once more (8 sequences of 16K: 38 us instead of 24).
+// After the block's attention: within it, the rare branch cost 1.0 us of 26 (8 sequences of up to 16K, int8).
+constexpr float kNear = 240.f, kFarScale = 0x1p40f, kFarLeast = 4096.f;
+__device__ __forceinline__ float item_value(float s, float m, float top) {
+    const float l = log2_fast(s), d = m - top;
+    if (s == 0.f) return kNegInf;
+    if (fabsf(m) <= kNear) return m + l;
+    const float v = l + d;
+    return (fabsf(v) < 0x1p-24f ? 0x1p-24f : v) * kFarScale;
+}
+__device__ __forceinline__ bool is_far(float v) { return fabsf(v) >= kFarLeast && v != kNegInf; }
+__device__ __forceinline__ void leave_weights(float *rec, volatile int *far, ItemSums w, const float *e, int n, int r,
+                                              int c) {
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) {
-        s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, sh);
-        s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, sh);
+        w.s0 += __shfl_xor_sync(0xFFFFFFFFu, w.s0, sh);
+        w.s1 += __shfl_xor_sync(0xFFFFFFFFu, w.s1, sh);
     }
-    if (r == 0) *reinterpret_cast<float2 *>(rec + 2 * c) = make_float2(m0 + log2_fast(s0), m1 + log2_fast(s1));
+    float2 v = make_float2(w.m0 + log2_fast(w.s0), w.m1 + log2_fast(w.s1));
+    if (__any_sync(0xFFFFFFFFu, fmaxf(fabsf(w.m0), fabsf(w.m1)) > kNear)) {
+        float top = kNegInf;
+        for (int i = r; i < n; i += 8) top = fmaxf(top, bias_log2(e[i]));
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, sh));
+        v = make_float2(item_value(w.s0, w.m0, top), item_value(w.s1, w.m1, top));
+        if (is_far(v.x) || is_far(v.y)) *far = 1;
+    }
+    if (r == 0) *reinterpret_cast<float2 *>(rec + 2 * c) = v;
 }
 
 // The item has nothing to attend: its weights are zero.
@@ -184,10 +215,11 @@ constexpr float kPBias = 14.f;  // e4m3: m is the running maximum less this
 
 // The softmax step of one block in a warp: x[i] holds slice i's logits (rows r and r + 8 of the slice,
 // heads 2c and 2c + 1) in the log2 domain.  Updates m and l, rescales o, leaves P in p.  kNan: NaN is
-// carried on; else it is passed over, as attend_block does.  bias: m is the maximum less this.
+// carried on; else it is passed over, as attend_block does.  bias: m is the maximum less this. ws (with kWeights):
+// the block's sums.
 template <bool kNan, bool kWeights, bool kF16>
-__device__ __forceinline__ void softmax_step(WarpState &st, float (&x)[4][4], uint32_t (&pb)[4][2], float bias, int r,
-                                             int c, float *rec) {
+__device__ __forceinline__ void softmax_step(WarpState &st, float (&x)[4][4], uint32_t (&pb)[4][2], float bias,
+                                             ItemSums &ws) {
     const auto row_max = [](float a, float b) { return kNan ? max_nan(a, b) : fmaxf(a, b); };
     float bm0 = row_max(x[0][0], x[0][2]), bm1 = row_max(x[0][1], x[0][3]);
 #pragma unroll
@@ -228,7 +260,7 @@ __device__ __forceinline__ void softmax_step(WarpState &st, float (&x)[4][4], ui
     st.l1 = fmaf(st.l1, c1, kWeights ? w1 : s1);
     st.m0 = mn0;
     st.m1 = mn1;
-    if constexpr (kWeights) leave_weights(rec, w0, w1, ms0, ms1, r, c);
+    if constexpr (kWeights) ws = ItemSums{w0, w1, ms0, ms1};
     if (__any_sync(0xFFFFFFFFu, c0 != 1.f || c1 != 1.f)) {  // the maximum rises a few times in a long context
 #pragma unroll
         for (int tt = 0; tt < 8; ++tt) {
@@ -243,7 +275,7 @@ __device__ __forceinline__ void softmax_step(WarpState &st, float (&x)[4][4], ui
 template <bool kWeights>
 __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtE4m3> &Q, const uint16_t *, int,
                                         const uint8_t *t, const float *eb, float sK, float sV, float qk_log2, int r,
-                                        int c, int sig, float *rec) {
+                                        int c, int sig, ItemSums &ws) {
     float x[4][4];
     // ---- S^T (4 slices of 16 tokens x 8 heads) ----
 #pragma unroll
@@ -272,7 +304,7 @@ __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtE4m3> &Q
         x[i][3] = fmaf(x[i][3], f1, eB);
     }
     uint32_t pb[4][2];
-    softmax_step<true, kWeights, true>(st, x, pb, kPBias, r, c, rec);
+    softmax_step<true, kWeights, true>(st, x, pb, kPBias, ws);
     // ---- O^T (128 dims x 8 heads) += s_V C'^T P^T ----
     float d[8][4];
 #pragma unroll
@@ -339,7 +371,7 @@ __device__ __forceinline__ void fourth_byte(float (&x)[4][4], const uint16_t *q,
 template <bool kWeights>
 __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtInt8> &Q, const uint16_t *q, int G,
                                         const uint8_t *t, const float *eb, float sK, float sV, float qk_log2, int r,
-                                        int c, int sig, float *rec) {
+                                        int c, int sig, ItemSums &ws) {
     // ---- S^T (4 slices of 16 tokens x 8 heads), a sum per byte of the queries ----
     float x[4][4];
 #pragma unroll
@@ -401,7 +433,7 @@ __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtInt8> &Q
         ph[i] = __byte_perm(lo, hi, 0x7531);
         pl[i] = __byte_perm(lo, hi, 0x6420);
     }
-    if constexpr (kWeights) leave_weights(rec, w0, w1, bs0, bs1, r, c);
+    if constexpr (kWeights) ws = ItemSums{w0, w1, bs0, bs1};
     const float mn0 = max_nan(st.m0, bm0), mn1 = max_nan(st.m1, bm1);
     const float ms0 = mn0 == kNegInf ? 0.f : mn0, ms1 = mn1 == kNegInf ? 0.f : mn1;
     const float c0 = exp2_fast(st.m0 - ms0), c1 = exp2_fast(st.m1 - ms1);
@@ -466,7 +498,7 @@ __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtInt8> &Q
 // at or beyond L are not seen.
 template <class Dims, bool kWeights>
 __device__ __forceinline__ void attend16(WarpState &st, const uint32_t (&qf)[8][2], const uint8_t *kt, const uint8_t *vt,
-                                         const float *eb, int32_t lb, int32_t L, float qk_log2, int r, int c, int sig, float *rec) {
+                                         const float *eb, int32_t lb, int32_t L, float qk_log2, int r, int c, int sig, ItemSums &ws) {
     constexpr bool kWide = std::is_same<Dims, Dims8>::value;  // chunks 2 sig, 2 sig + 1 of the row
     const int32_t n = min(L - lb * kBlock, kBlock);            // tokens seen
     float x[4][4];
@@ -494,7 +526,7 @@ __device__ __forceinline__ void attend16(WarpState &st, const uint32_t (&qf)[8][
         x[i][3] = rowB < n ? fmaf(x[i][3], qk_log2, eB) : kNegInf;
     }
     uint32_t pb[4][2];
-    softmax_step<kWide, kWeights, false>(st, x, pb, 0.f, r, c, rec);
+    softmax_step<kWide, kWeights, false>(st, x, pb, 0.f, ws);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (16 * i >= n) break;  // every P left is zero

@@ -127,13 +127,23 @@ __device__ __forceinline__ void merge_resident4(const DecodeParams &p, int32_t u
     merge_resident(p, u, h, d4 + 3, M, acc.w, lsum);
 }
 
+// A unit's whole softmax per head: the log2 of its sum, and where that is far from 0 its two parts.
+struct WholeSums {
+    float lse[kMaxG], M[kMaxG], l[kMaxG];
+    __device__ __forceinline__ void set(int h, float m, float sum) {
+        lse[h] = m + log2f(sum);
+        M[h] = m;
+        l[h] = sum;
+    }
+};
+
 // The last CTA of a unit merges the nc partial records src[], in order.  A thread takes 8 dims of a
 // head and has the loads of kBatch records in flight at once, since a round trip to the L2 (0.7 us) is
-// what this costs.  Writes bf16 out, or the merged record to res (the split decode's state); s_lse: the
-// log2 of each head's whole sum.
+// what this costs.  Writes bf16 out, or the merged record to res (the split decode's state), and the
+// heads' whole sums to *all.
 template <bool kNan>
 __device__ __forceinline__ void merge_records(const float *const *src, int nc, int G, uint16_t *out, float *res,
-                                              float *s_lse, int ctid) {
+                                              WholeSums *all, int ctid) {
     constexpr int kBatch = 4;
 #pragma unroll 1
     for (int v = ctid; v < G * (kD / 8); v += kItemConsThreads) {
@@ -186,38 +196,72 @@ __device__ __forceinline__ void merge_records(const float *const *src, int nc, i
             const uint2 lo = pack_out4<kNan>(a, ls), hi = pack_out4<kNan>(b, ls);
             *reinterpret_cast<uint4 *>(out + h * kD + d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
-        if (s_lse && d == 0) s_lse[h] = M + log2f(ls);
+        if (all && d == 0) all->set(h, M, ls);
     }
 }
 
-// A block's weight: its item's values (left by the warp that attended it) against the log2 of the
-// whole sums per head.
+// A block's weight: its item's values (left by the warp that attended it) against the whole sums per head.
 struct Weight {
-    int32_t lb;  // -1: none
+    int32_t lb, pb;  // the block's number (-1: none) and its place in the buffer
     float4 a, b;
 };
 
 __device__ __forceinline__ Weight load_weight(const DecodeParams &p, int32_t u, int32_t item0, int32_t n, int32_t j) {
     Weight w;
-    int32_t pb;
-    w.lb = -1;
+    w.lb = w.pb = -1;
     if (j >= n) return w;
     const float4 *rec = reinterpret_cast<const float4 *>(p.rec + (int64_t)(item0 + j) * kRecFloats);
     w.a = __ldcg(rec);
     w.b = __ldcg(rec + 1);
     const int32_t L = p.seq_len[u];
-    item_block(p, u, n - 1 - j, w.lb, pb);  // the items' order, see look_up
+    item_block(p, u, n - 1 - j, w.lb, w.pb);  // the items' order, see look_up
     if ((int64_t)w.lb * kBlock >= L) w.lb = -1;
     return w;
 }
 
-__device__ __forceinline__ void add_weight(const DecodeParams &p, int32_t u, const Weight &w, const float *s_lse) {
+// The largest of a block's logits in the log2 domain (n of its 64 are seen).  A call: it is wanted only where some
+// item's value is not plain, see leave_weights.
+__device__ __noinline__ float largest_logit(const float *e, int32_t n) {
+    float top = kNegInf;
+#pragma unroll 4
+    for (int i = 0; i < kBlock; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(e + i);
+        if (i < n) top = fmaxf(top, bias_log2(x.x));
+        if (i + 1 < n) top = fmaxf(top, bias_log2(x.y));
+        if (i + 2 < n) top = fmaxf(top, bias_log2(x.z));
+        if (i + 3 < n) top = fmaxf(top, bias_log2(x.w));
+    }
+    return top;
+}
+
+template <bool k8>
+__device__ __forceinline__ void add_weight(const DecodeParams &p, int32_t u, const Weight &w, const WholeSums &all,
+                                           bool far) {
     if (w.lb < 0) return;
     const float v[kMaxG] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
     float sum = 0.f;
+    if (far) {
+        float top = 0.f;
+        bool any = false;
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h)  // a head that sees nothing gives no weight
-        if (h < p.G && s_lse[h] != kNegInf) sum += exp2f(v[h] - s_lse[h]);
+        for (int h = 0; h < kMaxG; ++h) any |= is_far(v[h]);
+        if (any) {  // the logits, from where the attention read them
+            const int32_t L = p.seq_len[u];
+            const float *e = p.e + (int64_t)u * p.max_ctx + (int64_t)w.lb * kBlock;
+            if (k8 && w.lb < (L - 1) / kBlock)
+                e = reinterpret_cast<const float *>(
+                    p.records + ((int64_t)u * p.blocks_per_unit + w.pb) * kRec8Bytes + kBlock8Bytes);
+            top = largest_logit(e, L - w.lb * kBlock);
+        }
+#pragma unroll 1
+        for (int h = 0; h < p.G; ++h)
+            if (all.l[h] != 0.f)
+                sum += exp2f(is_far(v[h]) ? v[h] * (1.f / kFarScale) + (top - all.M[h]) : v[h] - all.M[h]) / all.l[h];
+    } else {
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h)  // a head that sees nothing gives no weight
+            if (h < p.G && all.lse[h] != kNegInf) sum += exp2f(v[h] - all.lse[h]);
+    }
     atomicAdd(p.weights + (int64_t)u * p.nblk + w.lb, sum);  // a caller's list may name a block twice
 }
 
@@ -256,7 +300,8 @@ __global__ void __launch_bounds__(kItemThreads, 1)
     __shared__ volatile int32_t s_tail_no[2];  // the tail last issued into each buffer
     __shared__ int s_last;
     __shared__ volatile int s_abort;
-    __shared__ float s_lse[kMaxG];
+    __shared__ WholeSums s_all;
+    __shared__ volatile int s_far;  // some item's weights of this CTA, or of one whose unit it ends, are not plain
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t U = p.units, grid = (int32_t)gridDim.x, cta = (int32_t)blockIdx.x;
@@ -276,6 +321,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             prefetch_tmap(&tmap);
             if (k8) prefetch_tmap(&tail_map);
             s_abort = 0;
+            s_far = 0;
         }
     }
     // ---- items of units < u ----
@@ -503,21 +549,23 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                         float *rec = kWeights ? p.rec + (int64_t)xi * kRecFloats : nullptr;
                         const uint8_t *t = tiles + s * kStageBytes;
                         const float *e = ebuf + s * kSide;
+                        [[maybe_unused]] ItemSums ws;
                         if (lb < 0) {
                             if (kWeights) leave_none(rec, r, c);
                         } else if constexpr (k8) {
                             if (tb >= 0) {
                                 load_q(u);  // once a unit
                                 attend16<Dims, kWeights>(st, qf, t, tails + tb * kHalfBlockBytes, e, lb, L, p.qk_log2,
-                                                         r, c, sig, rec);
+                                                         r, c, sig, ws);
                             } else {
                                 attend8<kWeights>(st, q8, p.q + (int64_t)u * p.G * kD, p.G, t, e, e[kBlock], e[kBlock + 1],
-                                                  p.qk_log2, r, c, sig, rec);
+                                                  p.qk_log2, r, c, sig, ws);
                             }
                         } else {
                             attend16<Dims, kWeights>(st, qf, t, t + kHalfBlockBytes, e, lb, L, p.qk_log2, r, c, sig,
-                                                     rec);
+                                                     ws);
                         }
+                        if (kWeights && lb >= 0) leave_weights(rec, &s_far, ws, e, min(L - lb * kBlock, kBlock), r, c);
                         __syncwarp();
                         if (lane == 0 && tb >= 0) mbar_arrive(&tempty[tb]);
                     }
@@ -538,7 +586,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 if (whole && !kResident) {
                     if (p.mode == kModeRest) merge_resident4(p, u, h, d4, M, acc, lsum);
                     *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<k8>(acc, lsum);
-                    if (kWeights && d4 == 0) s_lse[h] = M + log2f(lsum);
+                    if (kWeights && d4 == 0) s_all.set(h, M, lsum);
                 } else {
                     float *rec = whole ? p.res_part + (int64_t)u * kPartFloats : part;
                     *reinterpret_cast<float4 *>(rec + 2 * kMaxG + h * kD + d4) = acc;
@@ -554,12 +602,18 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 // semantics; the unit's last contributor acquired the others' partials with the same
                 // atomic, and the barrier after it orders every thread's later loads after them
                 const int32_t others = team > 0 ? team - 1 : cta_of((int64_t)u_end - 1, W, Ge) - cta_of(u_begin, W, Ge);
-                if (ctid == 0) s_last = (int32_t)atom_add_acq_rel_gpu(p.counter + u, 1u) == others;
+                // (with weights: and in the upper half, that some of the CTA's are not plain)
+                if (ctid == 0) {
+                    const uint32_t mine = kWeights && s_far ? 0x10001u : 1u;
+                    const uint32_t n = atom_add_acq_rel_gpu(p.counter + u, mine) + mine;
+                    s_last = (int32_t)(n & 0xFFFFu) == others + 1;
+                    if (kWeights && s_last && n >> 16) s_far = 1;
+                }
                 consumer_sync<kItemConsThreads>();
                 if (s_last) (slot == 0 ? last_first : last_other) = u;
             } else if (kWeights) {
                 for (int32_t j = ctid; j < u_end - u_begin; j += kItemConsThreads)
-                    add_weight(p, u, load_weight(p, u, u_begin, u_end - u_begin, j), s_lse);
+                    add_weight<k8>(p, u, load_weight(p, u, u_begin, u_end - u_begin, j), s_all, s_far);
                 consumer_sync<kItemConsThreads>();
             }
             x = seg_end;
@@ -592,13 +646,13 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             Weight w0;  // the first blocks' weights, in flight while the states are merged
             if (kWeights) w0 = load_weight(p, um, u_begin, u_end - u_begin, ctid);
             merge_records<k8>(src, nc, p.G, p.out + (int64_t)um * p.G * kD,
-                              kResident ? p.res_part + (int64_t)um * kPartFloats : nullptr, kWeights ? s_lse : nullptr,
+                              kResident ? p.res_part + (int64_t)um * kPartFloats : nullptr, kWeights ? &s_all : nullptr,
                               ctid);
             consumer_sync<kItemConsThreads>();
             if (kWeights) {
-                add_weight(p, um, w0, s_lse);
+                add_weight<k8>(p, um, w0, s_all, s_far);
                 for (int32_t j = ctid + kItemConsThreads; j < u_end - u_begin; j += kItemConsThreads)
-                    add_weight(p, um, load_weight(p, um, u_begin, u_end - u_begin, j), s_lse);
+                    add_weight<k8>(p, um, load_weight(p, um, u_begin, u_end - u_begin, j), s_all, s_far);
                 consumer_sync<kItemConsThreads>();
             }
         }

@@ -133,7 +133,7 @@ struct DecodeParams {
     int32_t fmt;                // kFmt* of the blocks
     const uint8_t *records;     // 8-bit store: the buffer of records (blocks_per_unit per unit)
     float *weights;             // [u][nblk] or null: each attended block's weight is added
-    float *rec;                 // with weights: [items][8 heads] log2 of the item's sum of 2^x
+    float *rec;                 // with weights: [items][8 heads], what leave_weights leaves of an item
 };
 
 constexpr int kRecFloats = kMaxG;  // one item's weights

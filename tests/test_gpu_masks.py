@@ -1,0 +1,81 @@
+"""Logits that are large or not finite: common offsets, masks by the lowest finite value, NaN.
+
+Every unit's block weights have to add up to its number of query heads, and `out` and the weights have to
+be of the same softmax, whatever lies on all of its logits.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_offloadable_b200 as nosa
+from tests import kv8_harness as H
+from tests import plain64 as P
+from tests.test_gpu_weights import check_weights
+
+pytestmark = pytest.mark.gpu
+FMTS = ["bf16", "int8", "e4m3"]
+LOWEST = np.finfo(np.float32).min
+
+# How far a unit's weights may be from adding up to its number of heads, relative to it.  A block's weight is
+# 2^(v - M) / l with v the log2 of its sum.  With q = 0, |v| relative to the block's largest logit is below 8: half a
+# step is 2^-22; log2, exp2, the 64 terms of the sum and 1 / l take 2^-22 each, the running sum l (up to 15 additions
+# of a warp, 13 states) 2^-20: below 2^-18.  With other queries |v| < 84, half a step 2^-18, ln 2 of it: below 2^-17.
+ZERO_Q, ANY_Q = 2.0 ** -18, 2.0 ** -17
+
+
+def offset_tokens(B, Hq, Hkv, L, offset, seed):
+    t = H.Tokens(B, Hq, Hkv, L, seed=seed)
+    t.e[:] = offset
+    return t
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("offset", [-1e4, -1e5, -1e6, -1e7, -1e9, 1e6, 1e9, LOWEST])
+def test_weights_add_up_under_a_common_offset(fmt, offset):
+    # units over many CTAs, one CTA a unit; all blocks and a selection
+    for B, L in ((1, 64 * 70 + 10), (100, 64 * 5 + 10)):
+        t = offset_tokens(B, 16, 2, L, offset, 41)
+        nblk = L // 64 + 2
+        lay = H.layer(t, nblk * 64, fmt, k_q=4, k_e=12, weights=True)
+        t.prefill(lay, L)
+        rows = np.append(np.full(L // 64, 64), [L % 64, 0])
+        out = torch.empty((B, 16, 128), dtype=torch.int16, device="cuda")
+        for zero in (True, False):
+            q = H.dev16(np.zeros_like(t.q()) if zero else t.q())
+            lay.weights.zero_()
+            lay.dense_decode_weights(q, out)
+            w = lay.weights.cpu().numpy().astype(np.float64)
+            assert np.abs(w.sum(1) - t.G).max() <= t.G * (ZERO_Q if zero else ANY_Q)
+            if zero:  # every token weighs the same
+                want = t.G * rows / L
+                assert (np.abs(w - want) <= ZERO_Q * want).all()
+            lay.weights.zero_()
+            lay.select(q)
+            lay.sparse_decode_weights(q, out)
+            w = lay.weights.cpu().numpy().astype(np.float64)
+            assert np.abs(w.sum(1) - t.G).max() <= t.G * (ZERO_Q if zero else ANY_Q)
+        assert lay.read_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("mask", [-1e9, -1e4, LOWEST, -np.inf])
+def test_weights_beside_masked_stretches(fmt, mask):
+    # the oldest blocks, the newest one, every other block, single tokens: what is left decides, to the usual bound
+    L = 64 * 21 + 30
+    t = H.Tokens(5, 8, 1, L, seed=42)
+    t.e[0, :64 * 9] = mask
+    t.e[1, 64 * 21:] = mask
+    t.e[2].reshape(-1)[:64 * 20].reshape(10, 128)[:, :64] = mask
+    t.e[3, 3::5] = mask
+    t.e[4, :L - 1] = mask
+    lay = H.layer(t, 64 * 23, fmt, weights=True)
+    t.prefill(lay, L)
+    units = [t.unit(u, L, fmt) for u in range(5)]
+    q = t.q()
+    q[:, 1] = P.to_bf16_bits(P.bf16(q[:, 1]) * 30)  # a head with logits far from the others'
+    out = torch.empty((5, 8, 128), dtype=torch.int16, device="cuda")
+    lay.dense_decode_weights(H.dev16(q), out)
+    got = lay.weights.cpu().numpy()
+    check_weights(t, got, np.zeros_like(got), q, units, [range(22)] * 5, 23)
+    H.check_out(t, out, q, units, [range(22)] * 5)
+    assert np.abs(got.sum(1) - 8).max() <= 8 * 2.0 ** -15  # the far head: |v| < 1024, half a step 2^-15
