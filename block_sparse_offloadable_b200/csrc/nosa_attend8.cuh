@@ -21,9 +21,10 @@
 // e4m3: every value is exact in f16, as is a bf16 query row once a power of two brings its largest
 // value to [2^14, 2^15): values down to 2^-31 of the largest keep every bit, smaller ones are off by at
 // most 2^-39 of it.  2^(x - m) goes to f16, 11 bits where the bf16 store's path has 8; m is kept 14
-// below the running maximum, so that the largest is 2^14 and the smallest normal one 2^-28 of it: a
-// token loses bits only below that, and is lost only below 2^-39 of the largest (2^20 tokens of that
-// size are 2^-19 of the sum).  The codes become f16 pairs by the conversion instruction.
+// below the running maximum, by the newest block (bf16) too, so that the largest is 2^14 and the smallest
+// normal one 2^-28 of it: a token loses bits only below that, and is lost only below 2^-39 of the largest
+// (2^20 tokens of that size are 2^-19 of the sum).  The codes become f16 pairs by the conversion
+// instruction.
 //
 // Layout.  One warp attends a whole block of 64 tokens, in four slices of 16: S^T = C Q^T and
 // O^T += C'^T P^T (attend_block gives a block to four warps).  The maximum, its two reductions over
@@ -496,7 +497,8 @@ __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtInt8> &Q
 // One bf16 block by one warp (kt: its key rows, vt: its value rows, two boxes each): the tail of an 8-bit store (Dims8: the value loads then have a two-way
 // bank conflict, on one block of a unit), or a block of the bf16 store whose weights are kept.  Tokens
 // at or beyond L are not seen.
-template <class Dims, bool kWeights>
+// kBias: softmax_step's, that of the unit's other blocks.
+template <class Dims, bool kWeights, bool kBias>
 __device__ __forceinline__ void attend16(WarpState &st, const uint32_t (&qf)[8][2], const uint8_t *kt, const uint8_t *vt,
                                          const float *eb, int32_t lb, int32_t L, float qk_log2, int r, int c, int sig, ItemSums &ws) {
     constexpr bool kWide = std::is_same<Dims, Dims8>::value;  // chunks 2 sig, 2 sig + 1 of the row
@@ -526,7 +528,7 @@ __device__ __forceinline__ void attend16(WarpState &st, const uint32_t (&qf)[8][
         x[i][3] = rowB < n ? fmaf(x[i][3], qk_log2, eB) : kNegInf;
     }
     uint32_t pb[4][2];
-    softmax_step<kWide, kWeights, false>(st, x, pb, 0.f, ws);
+    softmax_step<kWide, kWeights, false>(st, x, pb, kBias ? kPBias : 0.f, ws);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (16 * i >= n) break;  // every P left is zero

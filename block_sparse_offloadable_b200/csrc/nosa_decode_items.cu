@@ -555,15 +555,15 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                         } else if constexpr (k8) {
                             if (tb >= 0) {
                                 load_q(u);  // once a unit
-                                attend16<Dims, kWeights>(st, qf, t, tails + tb * kHalfBlockBytes, e, lb, L, p.qk_log2,
-                                                         r, c, sig, ws);
+                                attend16<Dims, kWeights, kFmt == kFmtE4m3>(st, qf, t, tails + tb * kHalfBlockBytes, e, lb,
+                                                                           L, p.qk_log2, r, c, sig, ws);
                             } else {
                                 attend8<kWeights>(st, q8, p.q + (int64_t)u * p.G * kD, p.G, t, e, e[kBlock], e[kBlock + 1],
                                                   p.qk_log2, r, c, sig, ws);
                             }
                         } else {
-                            attend16<Dims, kWeights>(st, qf, t, t + kHalfBlockBytes, e, lb, L, p.qk_log2, r, c, sig,
-                                                     ws);
+                            attend16<Dims, kWeights, false>(st, qf, t, t + kHalfBlockBytes, e, lb, L, p.qk_log2, r, c,
+                                                            sig, ws);
                         }
                         if (kWeights && lb >= 0) leave_weights(rec, &s_far, ws, e, min(L - lb * kBlock, kBlock), r, c);
                         __syncwarp();

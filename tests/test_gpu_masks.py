@@ -79,3 +79,36 @@ def test_weights_beside_masked_stretches(fmt, mask):
     check_weights(t, got, np.zeros_like(got), q, units, [range(22)] * 5, 23)
     H.check_out(t, out, q, units, [range(22)] * 5)
     assert np.abs(got.sum(1) - 8).max() <= 8 * 2.0 ** -15  # the far head: |v| < 1024, half a step 2^-15
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("how", ["dense", "sparse"])
+def test_small_weights_under_a_large_one_in_the_newest_block(fmt, how):
+    # one CTA attends a whole unit, the newest block first; the other tokens are 2^-26 of its largest, and alone
+    # have values.  Halves of f16 against that largest would lose them.
+    B, nb = 150, 16
+    L = 64 * nb + 10
+    t = H.Tokens(B, 1, 1, 1, seed=43)
+    t.k = np.zeros((B, L, 128), np.uint16)
+    t.e = np.full((B, L), -26 * np.log(2), np.float32)
+    t.e[:, L - 1] = 0
+    t.v = np.broadcast_to(P.to_bf16_bits(np.full(128, 64.0)), (B, L, 128)).copy()
+    t.v[:, 64 * nb:] = 0
+    lay = H.layer(t, 64 * (nb + 2), fmt, k_q=0, k_e=nb, weights=True)
+    t.prefill(lay, L)
+    q = t.q()
+    out = torch.empty((B, 1, 128), dtype=torch.int16, device="cuda")
+    if how == "dense":
+        lay.dense_decode(H.dev16(q), out)
+    else:
+        lay.select(H.dev16(q))
+        lay.sparse_decode(H.dev16(q), out)
+    got = H.out_of(out)
+    # 1024 weights of 2^-26 against 1 + 9 * 2^-26 + themselves.  P in 8, 11 or 16 bits of the same value: off by at
+    # most 2^-8 of it, as is the output's own rounding; the rest is below 2^-16.
+    p = np.exp(np.float64(t.e[0, 0]))
+    want = 64 * 64 * nb * p / (1 + (L - 1) * p)
+    assert np.abs(got - want).max() <= (2.0 ** -7 + 2.0 ** -16) * want
+    if how == "dense":
+        lay.dense_decode_weights(H.dev16(q), out)
+        assert np.abs(H.out_of(out) - want).max() <= (2.0 ** -7 + 2.0 ** -16) * want
