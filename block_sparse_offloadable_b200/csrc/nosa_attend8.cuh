@@ -215,25 +215,24 @@ __device__ __forceinline__ void load_query8(Query8<kFmt> &Q, const uint16_t *q, 
 constexpr float kPBias = 14.f;  // e4m3: m is the running maximum less this
 
 // The softmax step of one block in a warp: x[i] holds slice i's logits (rows r and r + 8 of the slice,
-// heads 2c and 2c + 1) in the log2 domain.  Updates m and l, rescales o, leaves P in p.  kNan: NaN is
-// carried on; else it is passed over, as attend_block does.  bias: m is the maximum less this. ws (with kWeights):
+// heads 2c and 2c + 1) in the log2 domain.  Updates m and l, rescales o, leaves P in p.  NaN is
+// carried on (attend_block passes over it).  bias: m is the maximum less this. ws (with kWeights):
 // the block's sums.
-template <bool kNan, bool kWeights, bool kF16>
+template <bool kWeights, bool kF16>
 __device__ __forceinline__ void softmax_step(WarpState &st, float (&x)[4][4], uint32_t (&pb)[4][2], float bias,
                                              ItemSums &ws) {
-    const auto row_max = [](float a, float b) { return kNan ? max_nan(a, b) : fmaxf(a, b); };
-    float bm0 = row_max(x[0][0], x[0][2]), bm1 = row_max(x[0][1], x[0][3]);
+    float bm0 = max_nan(x[0][0], x[0][2]), bm1 = max_nan(x[0][1], x[0][3]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
-        bm0 = row_max(bm0, row_max(x[i][0], x[i][2]));
-        bm1 = row_max(bm1, row_max(x[i][1], x[i][3]));
+        bm0 = max_nan(bm0, max_nan(x[i][0], x[i][2]));
+        bm1 = max_nan(bm1, max_nan(x[i][1], x[i][3]));
     }
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) {
-        bm0 = row_max(bm0, __shfl_xor_sync(0xFFFFFFFFu, bm0, sh));
-        bm1 = row_max(bm1, __shfl_xor_sync(0xFFFFFFFFu, bm1, sh));
+        bm0 = max_nan(bm0, __shfl_xor_sync(0xFFFFFFFFu, bm0, sh));
+        bm1 = max_nan(bm1, __shfl_xor_sync(0xFFFFFFFFu, bm1, sh));
     }
-    const float mn0 = row_max(st.m0, bm0 - bias), mn1 = row_max(st.m1, bm1 - bias);
+    const float mn0 = max_nan(st.m0, bm0 - bias), mn1 = max_nan(st.m1, bm1 - bias);
     const float ms0 = mn0 == kNegInf ? 0.f : mn0, ms1 = mn1 == kNegInf ? 0.f : mn1;  // nothing seen yet: all zeros
     const float c0 = exp2_fast(st.m0 - ms0), c1 = exp2_fast(st.m1 - ms1);
     float s0 = 0.f, s1 = 0.f;    // of P as it goes into the product: the denominator sums what the numerator sums
@@ -305,7 +304,7 @@ __device__ __forceinline__ void attend8(WarpState &st, const Query8<kFmtE4m3> &Q
         x[i][3] = fmaf(x[i][3], f1, eB);
     }
     uint32_t pb[4][2];
-    softmax_step<true, kWeights, true>(st, x, pb, kPBias, ws);
+    softmax_step<kWeights, true>(st, x, pb, kPBias, ws);
     // ---- O^T (128 dims x 8 heads) += s_V C'^T P^T ----
     float d[8][4];
 #pragma unroll
@@ -528,7 +527,7 @@ __device__ __forceinline__ void attend16(WarpState &st, const uint32_t (&qf)[8][
         x[i][3] = rowB < n ? fmaf(x[i][3], qk_log2, eB) : kNegInf;
     }
     uint32_t pb[4][2];
-    softmax_step<kWide, kWeights, false>(st, x, pb, kBias ? kPBias : 0.f, ws);
+    softmax_step<kWeights, false>(st, x, pb, kBias ? kPBias : 0.f, ws);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (16 * i >= n) break;  // every P left is zero

@@ -141,7 +141,6 @@ struct WholeSums {
 // head and has the loads of kBatch records in flight at once, since a round trip to the L2 (0.7 us) is
 // what this costs.  Writes bf16 out, or the merged record to res (the split decode's state), and the
 // heads' whole sums to *all.
-template <bool kNan>
 __device__ __forceinline__ void merge_records(const float *const *src, int nc, int G, uint16_t *out, float *res,
                                               WholeSums *all, int ctid) {
     constexpr int kBatch = 4;
@@ -193,7 +192,7 @@ __device__ __forceinline__ void merge_records(const float *const *src, int nc, i
                 res[kMaxG + h] = ls;
             }
         } else {
-            const uint2 lo = pack_out4<kNan>(a, ls), hi = pack_out4<kNan>(b, ls);
+            const uint2 lo = pack_out4<true>(a, ls), hi = pack_out4<true>(b, ls);
             *reinterpret_cast<uint4 *>(out + h * kD + d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
         if (all && d == 0) all->set(h, M, ls);
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 join_states<Dims, kTakers>(scratch, h, d4, M, acc, lsum);
                 if (whole && !kResident) {
                     if (p.mode == kModeRest) merge_resident4(p, u, h, d4, M, acc, lsum);
-                    *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<k8>(acc, lsum);
+                    *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<true>(acc, lsum);
                     if (kWeights && d4 == 0) s_all.set(h, M, lsum);
                 } else {
                     float *rec = whole ? p.res_part + (int64_t)u * kPartFloats : part;
@@ -645,7 +644,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
             consumer_sync<kItemConsThreads>();
             Weight w0;  // the first blocks' weights, in flight while the states are merged
             if (kWeights) w0 = load_weight(p, um, u_begin, u_end - u_begin, ctid);
-            merge_records<k8>(src, nc, p.G, p.out + (int64_t)um * p.G * kD,
+            merge_records(src, nc, p.G, p.out + (int64_t)um * p.G * kD,
                               kResident ? p.res_part + (int64_t)um * kPartFloats : nullptr, kWeights ? &s_all : nullptr,
                               ctid);
             consumer_sync<kItemConsThreads>();
@@ -671,7 +670,7 @@ __global__ void __launch_bounds__(kItemThreads, 1)
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 const int h = v / (kD / 4), d4 = (v % (kD / 4)) * 4;
                 if (p.mode == kModeRest) merge_resident4(p, uz, h, d4, M, acc, lsum);
-                *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<k8>(acc, lsum);
+                *reinterpret_cast<uint2 *>(out + h * kD + d4) = pack_out4<true>(acc, lsum);
             }
         }
         // the resident pass also leaves, per unit, the set it covered (for the rest pass)

@@ -398,9 +398,11 @@ int nosa_dense_decode(const nosa_config *cfg, const nosa_state *st, const uint16
  *   ws       device workspace of nosa_workspace_bytes(cfg, NOSA_WS_SPARSE_WEIGHTS) or
  *            (cfg, NOSA_WS_DENSE_WEIGHTS) bytes
  *
- * out as the plain calls write it.  Each block's total is one fp32 addition per call, in no
- * order that varies (a block that sel names once; nosa_select's never repeat).  The dense form wants
- * a device store, as nosa_dense_decode.
+ * out is the attention of the plain calls.  Over the bf16 store it is summed in another order, so its last
+ * bit may differ, and a head with a logit that is NaN gets NaN, in out as in the weights of the blocks that
+ * the call attends (the plain calls write zeros there; over the 8-bit store all calls give NaN).  Each
+ * block's total is one fp32 addition per call, in no order that varies (a block that sel names once;
+ * nosa_select's never repeat).  The dense form wants a device store, as nosa_dense_decode.
  */
 int nosa_sparse_decode_weights(const nosa_config *cfg, const nosa_state *st, const uint16_t *q, const int32_t *sel,
                                const int32_t *nsel, const int32_t *block_table, uint16_t *out, float *weights,

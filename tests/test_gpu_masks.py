@@ -112,3 +112,35 @@ def test_small_weights_under_a_large_one_in_the_newest_block(fmt, how):
     if how == "dense":
         lay.dense_decode_weights(H.dev16(q), out)
         assert np.abs(H.out_of(out) - want).max() <= (2.0 ** -7 + 2.0 ** -16) * want
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B", [1, 150])
+def test_nan_reaches_out_and_weights_alike(fmt, B):
+    # a key that is NaN: its unit's out and weights are; a value of the newest block: that dim of out alone; the
+    # other units as ever.  One CTA a unit, and many.
+    nb = 40 if B == 1 else 6
+    L = 64 * nb + 20
+    for where in ("none", "key", "newest key", "query", "newest value"):
+        t = H.Tokens(B, 4, 1, L, seed=44)
+        q = t.q()
+        if where == "key":
+            t.k[0, 70, 5] = 0x7FC0
+        elif where == "newest key":
+            t.k[0, L - 1, 5] = 0x7FC0
+        elif where == "newest value":
+            t.v[0, L - 1, 5] = 0x7FC0
+        elif where == "query":
+            q[0, :, 3] = 0x7FC0
+        lay = H.layer(t, 64 * (nb + 2), fmt, weights=True)
+        t.prefill(lay, L)
+        out = torch.empty((B, 4, 128), dtype=torch.int16, device="cuda")
+        lay.dense_decode_weights(H.dev16(q), out)
+        got, w = H.out_of(out), lay.weights.cpu().numpy()
+        if where in ("key", "newest key", "query"):
+            assert np.isnan(got[0]).all() and np.isnan(w[0, :nb + 1]).all(), where
+        else:
+            assert np.isnan(got[0, :, 5]).all() == (where == "newest value")
+            assert not np.isnan(np.delete(got[0], 5, 1)).any() and abs(w[0].sum() - 4) <= 4 * ANY_Q, where
+        assert not np.isnan(got[1:]).any() and not np.isnan(w[1:]).any()
+        assert not w[0, nb + 1:].any()
