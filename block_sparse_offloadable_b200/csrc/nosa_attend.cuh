@@ -42,6 +42,13 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
     return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
+// An eviction logit in the log2 domain.  The lowest finite floats would become -inf, which masks a
+// token outright: they stay finite, so that a row in which every token has such a mask is their mean.
+__device__ __forceinline__ float bias_log2(float e) {
+    constexpr float kLow = -2.3e38f;  // times log2(e): above the lowest float
+    return (e < kLow && e != kNegInf ? kLow : e) * kLog2e;
+}
+
 template <int kThreads = kConsThreads>
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
@@ -93,7 +100,7 @@ __device__ __forceinline__ void attend_block(WarpState &st, const uint32_t (&qf)
     for (int x = 0; x < 4; ++x) sacc[x] += sacc2[x];
     // ---- online softmax over the 16 tokens, per head (2c, 2c+1) ----
     const int64_t posA = (int64_t)lb * kBlock + rowA, posB = posA + 8;
-    const float eA = eb[rowA] * kLog2e, eB = eb[rowB] * kLog2e;
+    const float eA = bias_log2(eb[rowA]), eB = bias_log2(eb[rowB]);
     const float x0 = posA < L ? fmaf(sacc[0], qk_log2, eA) : kNegInf;
     const float x1 = posA < L ? fmaf(sacc[1], qk_log2, eA) : kNegInf;
     const float x2 = posB < L ? fmaf(sacc[2], qk_log2, eB) : kNegInf;

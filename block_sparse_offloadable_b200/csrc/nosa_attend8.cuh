@@ -38,13 +38,6 @@
 
 namespace nosa {
 
-// An eviction logit in the log2 domain.  The lowest finite floats would become -inf, which masks a
-// token outright: they stay finite, so that a row in which every token has such a mask is their mean.
-__device__ __forceinline__ float bias_log2(float e) {
-    constexpr float kLow = -2.3e38f;  // times log2(e): above the lowest float
-    return (e < kLow && e != kNegInf ? kLow : e) * kLog2e;
-}
-
 // The dims of a lane's accumulators: o[t][0..1] hold dim psi(t, sig) of heads 2c, 2c+1 and
 // o[t][2..3] dim psi(t, sig) + 1; at() places a dim in the merge scratch so that a warp's stores of
 // one t hit 32 distinct banks.

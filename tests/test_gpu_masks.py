@@ -144,3 +144,61 @@ def test_nan_reaches_out_and_weights_alike(fmt, B):
             assert not np.isnan(np.delete(got[0], 5, 1)).any() and abs(w[0].sum() - 4) <= 4 * ANY_Q, where
         assert not np.isnan(got[1:]).any() and not np.isnan(w[1:]).any()
         assert not w[0, nb + 1:].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B", [1, 150])
+def test_every_call_takes_a_mask_of_the_lowest_value_alike(fmt, B):
+    # a unit whose logits all are the lowest finite value is the mean of its values, whichever call attends it; with
+    # -inf beside it, of what is not -inf; -inf alone gives zeros.  tokens at the lowest value beside others: nothing.
+    nb = 40 if B == 1 else 5
+    L = 64 * nb + 20
+    for kind in ("lowest", "lowest and -inf", "-inf", "lowest and others"):
+        t = H.Tokens(B, 4, 1, L, seed=45)
+        t.e[:] = -np.inf if kind == "-inf" else LOWEST
+        seen = np.ones(L, bool)
+        if kind == "lowest and -inf":
+            seen[1::3] = False
+            t.e[:, ~seen] = -np.inf
+        if kind == "lowest and others":
+            seen[:] = np.arange(L) >= 64 * (nb - 1)
+            t.e[:, seen] = 0.5
+        q = t.q()
+        if kind == "lowest and others":
+            q[:] = 0  # every seen token weighs the same
+        lay = H.layer(t, 64 * (nb + 2), fmt, k_q=0, k_e=nb, weights=True)
+        t.prefill(lay, L)
+        units = [t.unit(u, L, fmt) for u in range(B)]
+        # equal weights: P is the same for all, the output is rounded once, the sums are off by 2^-16 of the mean |v|
+        want, size = (np.stack([f(r.v)[seen].mean(0) for r in units])[:, None] for f in (lambda x: x, np.abs))
+        tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * size
+        lay.select(H.dev16(q))
+        lay.decode_resident(H.dev16(q))
+        calls = {"dense": lay.dense_decode, "sparse": lay.sparse_decode, "split": lay.decode_rest,
+                 "dense weights": lay.dense_decode_weights, "sparse weights": lay.sparse_decode_weights}
+        for name, call in calls.items():
+            out = torch.full((B, 4, 128), 0x4242, dtype=torch.int16, device="cuda")
+            lay.weights.zero_()
+            call(H.dev16(q), out)
+            got = H.out_of(out)
+            if kind == "-inf":
+                assert not got.any() and not lay.weights.any(), name
+                continue
+            assert (np.abs(got - want) <= tol).all(), (kind, name, np.abs(got - want).max())
+            if name.endswith("weights"):
+                assert (lay.weights.sum(1) - 4).abs().max() <= 4 * ANY_Q, (kind, name)
+        assert lay.read_error() == 0
+
+
+def test_the_fused_step_takes_a_mask_of_the_lowest_value():
+    for B in (1, 150):
+        L = 64 * 9 + 20
+        t = H.Tokens(B, 4, 1, L + 1, seed=46)
+        t.e[:] = LOWEST
+        lay = H.layer(t, 64 * 11, "bf16", k_q=0, k_e=9)
+        t.prefill(lay, L)
+        out = torch.empty((B, 4, 128), dtype=torch.int16, device="cuda")
+        lay.fused_step(*t.new(np.full(B, L)), H.dev16(t.q()), out)
+        v = np.stack([t.unit(u, L + 1, "bf16").v for u in range(B)])
+        want = v.mean(1)[:, None]
+        assert (np.abs(H.out_of(out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * np.abs(v).mean(1)[:, None]).all()
