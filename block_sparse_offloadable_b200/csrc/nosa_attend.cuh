@@ -43,10 +43,11 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
 }
 
 // An eviction logit in the log2 domain.  The lowest finite floats would become -inf, which masks a
-// token outright: they stay finite, so that a row in which every token has such a mask is their mean.
+// token outright, and the largest +inf, which leaves NaN: both stay finite, so that a row in which every
+// token has the lowest value is their mean, and a token with the largest takes all of its row's weight.
 __device__ __forceinline__ float bias_log2(float e) {
-    constexpr float kLow = -2.3e38f;  // times log2(e): above the lowest float
-    return (e < kLow && e != kNegInf ? kLow : e) * kLog2e;
+    constexpr float kFar = 2.3e38f;  // times log2(e): a finite float
+    return (fabsf(e) > kFar && fabsf(e) != -kNegInf ? copysignf(kFar, e) : e) * kLog2e;
 }
 
 template <int kThreads = kConsThreads>

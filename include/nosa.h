@@ -375,8 +375,9 @@ int nosa_cache_sync(const nosa_config *cfg, const nosa_state *st, const int32_t 
  * For every query head h of kv head g: o_h = sum_j p_j v_j with
  * p = softmax_j(q_h . k_j * scale + e_j) over the tokens j < L of the blocks
  * in sel; bf16 inputs, fp32 accumulation, bf16 output (round to nearest even).
- * A logit e_j of -inf masks its token; where that leaves a unit nothing, o is zero.  Finite ones below
- * -2.3e38 count as -2.3e38, in every attention call: a unit with nothing else is the mean of those tokens.
+ * A logit e_j of -inf masks its token; where that leaves a unit nothing, o is zero.  Finite ones beyond
+ * -2.3e38 and 2.3e38 count as these, in every attention call: a unit with nothing but the lowest is the mean
+ * of its tokens.
  */
 int nosa_sparse_decode(const nosa_config *cfg, const nosa_state *st, const uint16_t *q,
                        const int32_t *sel, const int32_t *nsel, const int32_t *block_table,

@@ -202,3 +202,27 @@ def test_the_fused_step_takes_a_mask_of_the_lowest_value():
         v = np.stack([t.unit(u, L + 1, "bf16").v for u in range(B)])
         want = v.mean(1)[:, None]
         assert (np.abs(H.out_of(out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * np.abs(v).mean(1)[:, None]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("top", [2.5e38, np.finfo(np.float32).max])
+def test_a_logit_of_the_largest_values_takes_it_all(fmt, top):
+    L = 64 * 5 + 9
+    for at in (70, L - 2):
+        t = H.Tokens(3, 4, 1, L, seed=48)
+        t.e[0, at] = top
+        t.e[1] = LOWEST
+        t.e[1, at] = top
+        lay = H.layer(t, 64 * 7, fmt, k_q=0, k_e=5, weights=True)
+        t.prefill(lay, L)
+        units = [t.unit(u, L, fmt) for u in range(3)]
+        q = t.q()
+        lay.select(H.dev16(q))
+        for call in (lay.dense_decode, lay.sparse_decode, lay.dense_decode_weights):
+            out = torch.empty((3, 4, 128), dtype=torch.int16, device="cuda")
+            call(H.dev16(q), out)
+            for u in range(2):  # the value itself, rounded once (a code's: 2^-16 for its product and its weight)
+                want = units[u].v[at]
+                assert (np.abs(H.out_of(out)[u] - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want)).all(), (at, u)
+        w = lay.weights.cpu().numpy()
+        assert (np.abs(w[:2, at // 64] - 4) <= 4 * ANY_Q).all() and np.abs(w.sum(1) - 4).max() <= 4 * ANY_Q
