@@ -115,9 +115,16 @@ __device__ __forceinline__ void join_states(const float *scratch, int h, int d, 
     }
 }
 
-// merge_resident for dims d4 .. d4 + 3.
+// merge_resident for dims d4 .. d4 + 3.  Where neither state has a maximum, both are empty or NaN, and NaN is carried on.
 __device__ __forceinline__ void merge_resident4(const DecodeParams &p, int32_t u, int h, int d4, float &M, float4 &acc,
                                                 float &lsum) {
+    const float *res = p.res_part + (int64_t)u * kPartFloats;
+    if (M == kNegInf && res[h] == kNegInf) {
+        const float4 o = *reinterpret_cast<const float4 *>(res + 2 * kMaxG + h * kD + d4);
+        acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+        lsum += res[kMaxG + h];
+        return;
+    }
     float m = M, l = lsum;
     merge_resident(p, u, h, d4, m, acc.x, l);
     m = M, l = lsum;

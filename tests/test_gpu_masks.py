@@ -226,3 +226,21 @@ def test_a_logit_of_the_largest_values_takes_it_all(fmt, top):
                 assert (np.abs(H.out_of(out)[u] - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want)).all(), (at, u)
         w = lay.weights.cpu().numpy()
         assert (np.abs(w[:2, at // 64] - 4) <= 4 * ANY_Q).all() and np.abs(w.sum(1) - 4).max() <= 4 * ANY_Q
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("L", [5, 64 * 3 + 7])
+def test_split_attention_carries_nan(fmt, L):
+    # all that the unit attends is resident and NaN, and the second pass has nothing to add: NaN, as in one pass
+    t = H.Tokens(2, 4, 1, L, seed=47)
+    q = t.q()
+    q[0, :, 3] = 0x7FC0
+    lay = H.layer(t, 64 * 5, fmt, k_q=2, k_e=4)
+    t.prefill(lay, L)
+    one, two = (torch.empty((2, 4, 128), dtype=torch.int16, device="cuda") for _ in range(2))
+    lay.decode_resident(H.dev16(q))
+    lay.select(H.dev16(q))
+    lay.decode_rest(H.dev16(q), two)
+    lay.sparse_decode(H.dev16(q), one)
+    assert np.isnan(H.out_of(one)[0]).all() and np.isnan(H.out_of(two)[0]).all()
+    assert not np.isnan(H.out_of(two)[1]).any()
