@@ -278,7 +278,9 @@ class NosaLayer:
     ``host_store``: in offload mode, an existing pinned uint8 tensor to use as the host KV store
     (several layers may share one when their synthetic KV is identical); allocated if None.
     ``weights``: keep a running total of each block's attention weight (``self.weights`` fp32
-    [units][blocks]); ``decode_step`` then adds to it.
+    [units][blocks]); ``decode_step``, ``sparse_decode_weights`` and ``dense_decode_weights`` add to it.
+    ``sparse_decode``, ``dense_decode``, ``decode_resident`` + ``decode_rest`` and ``fused_step`` do not,
+    in such a layer either.
     """
 
     def __init__(self, cfg, device="cuda", host_store=None, weights=False):

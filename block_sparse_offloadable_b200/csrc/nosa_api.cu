@@ -458,7 +458,7 @@ int make_select(const nosa_config *c, const nosa_state *st, const uint16_t *q, i
     p.k8 = fmt_of(c) != kFmtBf16;
     // A large launch's pooled keys would push out of L2 what the attention over codes needs again, its
     // instructions above all: append + select and decode of a layer, 32 x 32K (68 MB of keys), int8:
-    // 45.7 us, 42.2 where the keys go first; 4 x 32K (9 MB), all in L2: 24.3 and 25.4.
+    // 45.7 us, 42.2 where the keys go first; 4 x 32K (9 MB), all in L2: 24.3 and 25.4 (graph replays).
     p.once = p.k8 && nosa_state_bytes(c, NOSA_BUF_CK) > kL2Bytes / 4;
     p.fill = (c->flags & NOSA_FLAG_FILL) != 0;
     p.pool = p.fill ? st->pool : nullptr; p.pool_n = p.fill ? st->pool_n : nullptr;

@@ -202,8 +202,9 @@ __device__ __forceinline__ void code_block(const uint4 (&k)[4], const uint4 (&v)
 // codes; the keys also go to shared memory, where the pooled means are summed (thread = sub-block
 // and pair of dims, in row order).  The newest block's rows go to the tail as they are.  Reads
 // 33 KiB and writes 19 KiB a block; bound by HBM.  The keys are coded from shared memory: 40 registers,
-// six CTAs an SM.  32 sequences of up to 32K (2 kv heads, bf16 pooled keys), the whole call: 204 us, 0.93
-// of the measured HBM rate; coded from registers 221 (four CTAs), 216 to 220 (five), 227 to 231 (six,
+// six CTAs an SM.  32 sequences of up to 32K (2 kv heads, bf16 pooled keys), with the state's init and
+// Gamma_e, replayed from a graph: 201 to 209 us, 0.91 to 0.95 of the measured HBM rate (as calls 223 to 230, 0.83
+// to 0.85); coded from registers 221 (four CTAs), 216 to 220 (five), 227 to 231 (six,
 // spills); with streaming stores 230.
 __global__ void __launch_bounds__(256, 6) prefill_store8_kernel(const AppendParams p) {
     __shared__ __align__(16) uint8_t ks[kHalfBlockBytes];

@@ -12,14 +12,15 @@
 //  * One consumer warp attends a whole block (nosa_attend8.cuh).  Five of them (three over the bf16
 //    store) with two stages each: a stage's next block is in flight while its other one is
 //    attended.  Eight warps with ten stages leave two blocks in flight while all attend: 93 us at
-//    32 ragged sequences of up to 32K (e4m3, 16 q / 2 kv heads) where five warps took 75 (70 now,
-//    0.89 of the measured HBM rate).
+//    32 ragged sequences of up to 32K (e4m3, 16 q / 2 kv heads) where five warps took 75 (70.3 now,
+//    0.89 of the measured HBM rate; 76 as calls one after the other, 0.83).
 //  * Two producer warps, for the even and the odd items: one issue (expected bytes, a tensor copy of
 //    the codes, a bulk copy of the logits and scales) takes 0.27 us of one thread's time, and a
 //    block must come every 0.38 us to keep the memory busy; the first items are issued by the
 //    consumer warps and the producers at once.
 //  * The newest block of a unit (bf16 tail of the 8-bit store) takes longest and comes first.
 //  * Seven warps leave 255 registers a thread: attend8 wants about 200.
+// Times in these files are replays of a captured graph over several states, unless they say calls.
 #include "nosa_attend8.cuh"
 #include "nosa_decode_work.cuh"
 
@@ -382,8 +383,11 @@ __global__ void __launch_bounds__(kItemThreads, 1)
     if (p.pieces <= 0 && U <= 32 && U <= Ge && W > 0) {
         // Few units, of any lengths: a CTA for each and the others in proportion to the units' items, equal
         // pieces of a unit each, if that gives no CTA more than kAlignItems items more than balanced
-        // ranges.  It spares ranges with two units in them, whose first one's end holds up the stream (16
-        // units of 129 to 257 blocks, with weights: 24.2 us, balanced 27.7).
+        // ranges.  It spares ranges with two units in them, whose first one's end holds up the stream.
+        // int8 with weights, units of 129 to 257 blocks, against balanced ranges: 16 units 23.7 us (27.4), 24
+        // units 28.8 (31.5), 32 units 35.7 (35.2); 32 units of 33 to 65 blocks 16.7 (21.2).  A warp holds 32
+        // units, and there the gain ends where the units are long.  Balanced, 40 units take 39.0 (bytes alone
+        // 20.3), 100 units 71.5 (51.9).
         const int32_t n = lane < U ? first_item(lane + 1) - first_item(lane) : 0;
         const int32_t mine = n > 0 ? 1 + (int32_t)((int64_t)n * (Ge - U) / W) : 0;  // Ge in all at most
         const int32_t most = (int32_t)__reduce_max_sync(0xFFFFFFFFu, n > 0 ? (uint32_t)((n + mine - 1) / mine) : 0u);

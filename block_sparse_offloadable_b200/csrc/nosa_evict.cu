@@ -15,8 +15,8 @@
 // has once (lengths, Gamma_e and the pool renumbered, weights).  move: a CTA per kept block copies its
 // rows or codes, logits, pooled keys and score; only what the unit's tokens have filled is read or
 // written.  Bound by HBM: every kept byte is read and written once.  Measured: 16 units of 512 blocks,
-// 64 kept, bf16: 21.7 us; 64 units of up to 256 blocks, 128 kept, int8: 57 us, 0.83 of the measured HBM
-// rate.  One kernel in which teams of CTAs choose and then copy, each its share: 26.5 and 99.9 us (a CTA's
+// 64 kept, bf16: 21.8 us; 64 units of up to 256 blocks, 128 kept, int8: 56 us, 0.84 of the measured HBM
+// rate (both as calls within 2 %).  One kernel in which teams of CTAs choose and then copy, each its share: 26.5 and 99.9 us (a CTA's
 // blocks one after the other leave too little in flight).
 #include "nosa_internal.cuh"
 #include "nosa_topk.cuh"

@@ -118,7 +118,8 @@ typedef struct nosa_config {
  * over the block gives NaN.  The newest (local) block of a unit is held in bf16 in the unit's tail,
  * and coded once, when the first token of the next block arrives.  Pooled keys and eviction scores
  * are those of the bf16 input.  Every call works with these flags but nosa_fused_step
- * (NOSA_ERR_UNSUPPORTED); a missed block is 16656 bytes to fetch, not 32768.
+ * (NOSA_ERR_UNSUPPORTED); a missed block is 16656 bytes to fetch, not 32768.  Small steps, which wait on
+ * launches and not on bytes, are faster over the bf16 store with nosa_fused_step.
  */
 #define NOSA_FLAG_KV_INT8 0x8
 #define NOSA_FLAG_KV_E4M3 0x10
@@ -134,7 +135,9 @@ typedef struct nosa_config {
  *               of its keys and of its values, and 120 bytes unused.  Behind the records, in the buffer that
  *               is device memory (here if offload == 0), from the next multiple of 256 bytes
  *               on: the tails, bf16 [u][2][64][D]
- *   evict_logit fp32 [u][max_ctx]   per-token eviction logit e_j (device)
+ *   evict_logit fp32 [u][max_ctx]   per-token eviction logit e_j (device).  With NOSA_FLAG_KV_INT8 / _E4M3
+ *               attention reads the newest block's here and a coded block's from its record, a copy made
+ *               when the block was coded: a later change here does not reach it
  *   ck          fp32 [u][nsub][D]   compressed keys: mean of each 16-token sub-block (device);
  *               bf16 [u][nsub][D] with NOSA_FLAG_CK_BF16
  *   blk_evict   fp64 [u][nblk]      block eviction score E_b, pre-exponential (device)
@@ -397,7 +400,9 @@ int nosa_dense_decode(const nosa_config *cfg, const nosa_state *st, const uint16
  *
  *   weights  device fp32 [u][nblk], in/out: weights[u][b] += sum over the G query heads of kv head g
  *            and over the tokens j of block b of softmax_j(q_h . k_j * scale + e_j).  Blocks that
- *            the call does not attend are left as they are.  Zero it when the sequences start.
+ *            the call does not attend are left as they are, and no other call adds to them (not
+ *            nosa_sparse_decode, nosa_dense_decode, nosa_decode_resident / _rest or
+ *            nosa_fused_step).  Zero it when the sequences start.
  *   ws       device workspace of nosa_workspace_bytes(cfg, NOSA_WS_SPARSE_WEIGHTS) or
  *            (cfg, NOSA_WS_DENSE_WEIGHTS) bytes
  *

@@ -7,7 +7,6 @@ import numpy as np
 import pytest
 import torch
 
-import block_sparse_offloadable_b200 as nosa
 from tests import kv8_harness as H
 from tests import plain64 as P
 from tests.test_gpu_weights import check_weights
@@ -244,3 +243,32 @@ def test_split_attention_carries_nan(fmt, L):
     lay.sparse_decode(H.dev16(q), one)
     assert np.isnan(H.out_of(one)[0]).all() and np.isnan(H.out_of(two)[0]).all()
     assert not np.isnan(H.out_of(two)[1]).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("offset", [-1e9, LOWEST])
+def test_weights_add_up_over_the_block_cache(fmt, offset):
+    # the same under an offset where the blocks' logits lie in cache slots, and replayed from a graph
+    L, steps = 64 * 9 + 62, 4
+    t = offset_tokens(3, 8, 2, L + steps, offset, 49)
+    lay = H.layer(t, 64 * 12, fmt, k_q=2, k_e=3, offload=True, weights=True)
+    t.prefill(lay, L)
+    q = H.dev16(t.q())
+    k, v, e = t.new(np.full(t.units, L))
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        lay.decode_step(k, v, e, q, out)
+    for i in range(steps):  # over the border at 64 * 10
+        for dst, src in zip((k, v, e), t.new(np.full(t.units, L + i))):
+            dst.copy_(src)
+        before = lay.weights.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.replay()
+        torch.cuda.synchronize()
+        gain = (lay.weights - before).cpu().numpy().astype(np.float64)
+        # a total's own addition: half a step of it for each of at most 6 blocks
+        assert np.abs(gain.sum(1) - t.G).max() <= t.G * ANY_Q + 6 * 2.0 ** -24 * float(lay.weights.max()), i
+    assert lay.read_error() == 0
